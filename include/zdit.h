@@ -8,7 +8,10 @@
  *     blocks and the final layer (zdit_stack_forward),
  *   - the fused negated-CFG FlowMatchEuler update (zdit_euler_cfg_step),
  * plus the pieces those are made of, exposed so they can be checked one by one
- * (joint attention, the projection GEMM, RoPE tables, patchify).
+ * (joint attention, the projection GEMM, RoPE tables, patchify), and the operators of
+ * the causal transformer that turns prompts into the caption features the DiT reads:
+ * scaled rotary tables, per-head query / key norm with rotation, causal attention with
+ * grouped heads over packed prompts, and projections with a fused epilogue.
  *
  * Sources for what is computed (web pages, by title and section):
  *   [CoreAI] "Z-Image-Turbo port - a 6B diffusion DiT on Core AI, and why it is
@@ -358,6 +361,167 @@ ZDIT_API zdit_status zdit_adaln_project(const void* const* w_ada, const float* c
  * ZDIT_ERR_CUDA. */
 ZDIT_API zdit_status zdit_gemm_bf16(const void* A, const void* B, float* C, int64_t M, int64_t N, int64_t K,
                                     int64_t ldc, const float* bias, void* stream);
+
+/* ------------------------------------------------------------------ prompt operators
+ * The layers of a causal transformer over prompt tokens (the encoder whose last hidden
+ * rows are the DiT's cap_feats, [CoreAI] pipeline table) need, beside the projection GEMM:
+ * rotary tables of one position per token, per-head norms with either pairing of the
+ * rotation, attention that is causal, has fewer key heads than query heads and runs over
+ * prompts of different lengths packed one after the other, and projections that add
+ * bias, activation and residual.  The four calls below are forward only, like the rest
+ * of the library. */
+
+/* Element types of the buffers whose type a call leaves open. */
+enum { ZDIT_T_BF16 = 0, ZDIT_T_F32 = 1 };
+
+/* Rows of heads: element d of head h of row t is ptr[t * row_stride + h * head_stride + d].
+ * Strides in elements.  Token-major rows (q inside a projection's q | k | v row:
+ * head_stride = head_dim, row_stride = the whole row) and head-major caches
+ * (row_stride = head_dim, head_stride = capacity * head_dim) are both of this form. */
+typedef struct {
+  void* ptr;
+  int64_t row_stride;
+  int64_t head_stride;
+} zdit_heads;
+
+/* How the frequencies w_i = theta^(-2i/d), i < d/2, d = rotary_dim, are scaled for
+ * sequences longer than the trained ones:
+ *   NONE    w_i
+ *   LINEAR  w_i / factor                                  (positions interpolated)
+ *   NTK     (theta factor^(d/(d-2)))^(-2i/d)               (base enlarged; d > 2)
+ *   YARN    w_i (g_i + (1 - g_i) / factor), g_i = clamp((r_i - beta_slow) /
+ *           (beta_fast - beta_slow), 0, 1), r_i = original_len w_i / 2 pi turns over the
+ *           trained length (interpolation "by parts", the ramp taken in turns as the
+ *           YaRN paper defines it)
+ * magnitude multiplies cos and sin (1: plain rotation; the attention temperature of the
+ * by-parts method otherwise). */
+enum { ZDIT_ROPE_SCALE_NONE = 0, ZDIT_ROPE_SCALE_LINEAR = 1, ZDIT_ROPE_SCALE_NTK = 2, ZDIT_ROPE_SCALE_YARN = 3 };
+typedef struct {
+  int32_t kind;        /* ZDIT_ROPE_SCALE_*                                       */
+  float factor;        /* >= 1; ignored by NONE                                   */
+  float original_len;  /* > 0; YARN only                                          */
+  float beta_fast;     /* YARN only, beta_fast > beta_slow >= 0                    */
+  float beta_slow;
+  float magnitude;     /* > 0, all kinds                                          */
+} zdit_rope_scaling;
+
+/* cos_out[t, i] = magnitude cos(pos[t] w_i), sin_out alike; device fp32 [T, rotary_dim / 2].
+ *   pos         device int32 [T], any value (angles are formed and reduced in double
+ *               precision, so positions far past 2^24 keep their phase)
+ *   rotary_dim  even, 2..512;  theta >= 1 (frequencies at most 1)
+ *   scaling     NULL: NONE with magnitude 1
+ * T == 0 does nothing.  Errors: ZDIT_ERR_INVALID_ARG (null pointers, theta, scaling
+ * values), ZDIT_ERR_SHAPE, ZDIT_ERR_ALIGNMENT (cos_out, sin_out 16-byte aligned),
+ * ZDIT_ERR_CUDA. */
+ZDIT_API zdit_status zdit_rope_table_scaled(const int32_t* pos, int64_t T, int32_t rotary_dim, float theta,
+                                            const zdit_rope_scaling* scaling, float* cos_out, float* sin_out,
+                                            void* stream);
+
+/* Pairing of the rotation: elements (2i, 2i + 1), or (i, i + rotary_dim / 2). */
+enum { ZDIT_ROPE_INTERLEAVED = 0, ZDIT_ROPE_HALF = 1 };
+
+/* Per-head norm of queries and keys and their rotation, one pass:
+ *   x <- x / sqrt(mean(x^2) + eps) * w     (w_q for queries, w_k for keys; NULL: no norm)
+ *   (a, b) <- (a cos_i - b sin_i, a sin_i + b cos_i) for pair i < rotary_dim / 2
+ * computed in fp32 and rounded once; elements past rotary_dim are only normed.
+ *   q, k          in_dtype, T rows of n_q / n_k heads; n_k == 0: queries only
+ *   q_out, k_out  out_dtype.  The same buffer as the input (pointer, strides and type
+ *                 alike: in place) or one that does not overlap it.
+ *   head_dim      a multiple of 8, 8..256
+ *   w_q, w_k      device fp32 [head_dim] or NULL, 16-byte aligned
+ *   cos, sin      device fp32 [T, rotary_dim / 2], 16-byte aligned; may be NULL if
+ *                 rotary_dim == 0
+ *   rotary_dim    even, 0..head_dim
+ * Pointers of heads 16-byte aligned, strides multiples of 16 bytes, heads and rows of an
+ * output not overlapping one another.  T == 0 does nothing.  Errors: ZDIT_ERR_INVALID_ARG,
+ * ZDIT_ERR_SHAPE, ZDIT_ERR_ALIGNMENT, ZDIT_ERR_CUDA. */
+typedef struct {
+  int64_t T;
+  int32_t n_q, n_k, head_dim;
+  int32_t in_dtype, out_dtype; /* ZDIT_T_*                                        */
+  zdit_heads q, k, q_out, k_out;
+  const float* w_q;
+  const float* w_k;
+  float eps;
+  const float* cos;
+  const float* sin;
+  int32_t rotary_dim;
+  int32_t layout; /* ZDIT_ROPE_INTERLEAVED or ZDIT_ROPE_HALF */
+} zdit_qk_norm_rope_args;
+ZDIT_API zdit_status zdit_qk_norm_rope(const zdit_qk_norm_rope_args* a, void* stream);
+
+/* Attention of packed prompts with grouped heads.  Sequence b owns the q_len[b] query rows
+ * that follow those of sequence b - 1 (the first starts at row 0 of q and o) and the
+ * kv_len[b] key rows from row kv_start[b] of k and v:
+ *   O_i = sum_j p_ij V_j, p_i = softmax over the allowed j of scale * q_i . k_j
+ * with j allowed when j <= i + kv_len[b] - q_len[b] (causal: the last query row sees every
+ * key, so q_len < kv_len is the new part of a kept prefix and q_len == 1 a single token) or
+ * always (not causal).  Query head h reads key head h / (n_heads / n_kv_heads).  A row that
+ * no key is allowed for (q_len > kv_len, kv_len == 0) becomes zeros.
+ *   q, o   bf16, sum(q_len) rows of n_heads; o does not overlap q, k or v; rows of o past
+ *          the last sequence are not written
+ *   k, v   bf16, n_kv_heads; sequences may share rows or leave gaps; rows of no sequence
+ *          are never used, whatever they hold (NaN included).  Rows that a sequence does
+ *          own have to hold finite values: keys are taken 128 at a time, so an infinity or
+ *          NaN in a row of v reaches query rows of the same sequence that come before it.
+ *   q_len, kv_len, kv_start  HOST int32 [batch], read during the call only, values >= 0.
+ *          kv_len NULL: q_len; kv_start NULL: sequences packed one after the other.
+ *          A captured launch keeps the lengths it was captured with.
+ *   batch 1..128, n_heads a multiple of n_kv_heads with a quotient of at most 64,
+ *   head_dim 64 or 128; scale > 0 and finite (0: 1 / sqrt(head_dim)).
+ * Pointers 16-byte aligned, strides multiples of 8 elements and at least head_dim where
+ * there is more than one head or row, heads and rows of o not overlapping one another.
+ * The key axis is split over several CTAs when the rows alone do not fill the GPU; the
+ * parts are joined from the workspace in a fixed order (results do not depend on timing).
+ *   workspace  device, 256-byte aligned, >= zdit_prompt_attention_workspace_bytes (0 when
+ *              nothing is split: then it may be NULL).  Calls that overlap on the GPU need
+ *              workspaces of their own, captured graphs that may run at once too.
+ * Errors: ZDIT_ERR_INVALID_ARG, ZDIT_ERR_SHAPE, ZDIT_ERR_ALIGNMENT, ZDIT_ERR_WORKSPACE,
+ * ZDIT_ERR_CUDA. */
+typedef struct {
+  int32_t batch;
+  const int32_t* q_len;
+  const int32_t* kv_len;
+  const int32_t* kv_start;
+  int32_t n_heads, n_kv_heads, head_dim;
+  int32_t causal; /* 0 or 1 */
+  float scale;
+  zdit_heads q, k, v, o;
+} zdit_prompt_attention_args;
+/* Only batch, the lengths, the head counts, head_dim and causal are read; 0 on invalid ones. */
+ZDIT_API size_t zdit_prompt_attention_workspace_bytes(const zdit_prompt_attention_args* a);
+ZDIT_API zdit_status zdit_prompt_attention(const zdit_prompt_attention_args* a, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/* Projection with its epilogue: out = residual + act(a . w^T + bias), fp32 accumulation,
+ * rounded once when it is stored.
+ *   a          bf16 [M, K], row stride lda;  w  bf16 [N, K], row stride ldw
+ *   bias       device fp32 [N] or NULL
+ *   act        ZDIT_ACT_* (GELU: y Phi(y); GELU_TANH: its tanh form)
+ *   residual   residual_dtype [M, N], row stride ld_residual, or NULL; may be out itself
+ *              (pointer, stride and type alike), otherwise does not overlap it
+ *   out        out_dtype [M, N], row stride ld_out
+ * Any M >= 0, N, K >= 1.  a and w 16-byte aligned with strides that are multiples of 8
+ * elements (K need not be); bias, residual and out aligned to their element.  Columns past
+ * K and rows past M or N are never used.  Errors: ZDIT_ERR_INVALID_ARG, ZDIT_ERR_SHAPE,
+ * ZDIT_ERR_ALIGNMENT, ZDIT_ERR_CUDA. */
+enum { ZDIT_ACT_NONE = 0, ZDIT_ACT_SILU = 1, ZDIT_ACT_GELU_TANH = 2, ZDIT_ACT_GELU = 3 };
+typedef struct {
+  int64_t M, N, K;
+  const void* a;
+  int64_t lda;
+  const void* w;
+  int64_t ldw;
+  const float* bias;
+  int32_t act;
+  const void* residual;
+  int64_t ld_residual;
+  int32_t residual_dtype; /* ZDIT_T_* */
+  void* out;
+  int64_t ld_out;
+  int32_t out_dtype; /* ZDIT_T_* */
+} zdit_linear_args;
+ZDIT_API zdit_status zdit_linear(const zdit_linear_args* a, void* stream);
 
 /* Patchify a latent [C, 2h, 2w] (device fp32) into tokens [h*w, 4C] (device fp32),
  * token n = hi * w + wi, feature f = (dy * 2 + dx) * C + c ([CoreAI] "Hosting it

@@ -21,6 +21,9 @@ STATUS = {0: "ZDIT_OK", -1: "ZDIT_ERR_INVALID_ARG", -2: "ZDIT_ERR_SHAPE", -3: "Z
           -7: "ZDIT_ERR_DEVICE_TIMEOUT"}
 
 F_ADALN, F_SANDWICH_NORM, F_QK_NORM, F_TANH_GATE = 1, 2, 4, 8
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_YARN = 0, 1, 2, 3
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1
+ACT_NONE, ACT_SILU, ACT_GELU_TANH, ACT_GELU = 0, 1, 2, 3
 
 
 class ZditError(RuntimeError):
@@ -76,6 +79,43 @@ class ProfileEntry(C.Structure):
                 ("flops", C.c_double), ("bytes", C.c_double)]
 
 
+class RopeScaling(C.Structure):
+    """Frequency scaling of zdit_rope_table_scaled: RopeScaling(kind, factor, original_len,
+    beta_fast, beta_slow, magnitude); the trailing values default to those of no scaling."""
+    _fields_ = [("kind", C.c_int32), ("factor", C.c_float), ("original_len", C.c_float),
+                ("beta_fast", C.c_float), ("beta_slow", C.c_float), ("magnitude", C.c_float)]
+
+    def __init__(self, kind=ROPE_SCALE_NONE, factor=1.0, original_len=1.0, beta_fast=32.0, beta_slow=1.0,
+                 magnitude=1.0):
+        super().__init__(kind, factor, original_len, beta_fast, beta_slow, magnitude)
+
+
+class Heads(C.Structure):
+    _fields_ = [("ptr", C.c_void_p), ("row_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class QkNormRopeArgs(C.Structure):
+    _fields_ = [("T", C.c_int64), ("n_q", C.c_int32), ("n_k", C.c_int32), ("head_dim", C.c_int32),
+                ("in_dtype", C.c_int32), ("out_dtype", C.c_int32), ("q", Heads), ("k", Heads),
+                ("q_out", Heads), ("k_out", Heads), ("w_q", C.c_void_p), ("w_k", C.c_void_p),
+                ("eps", C.c_float), ("cos", C.c_void_p), ("sin", C.c_void_p), ("rotary_dim", C.c_int32),
+                ("layout", C.c_int32)]
+
+
+class PromptAttentionArgs(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("q_len", C.POINTER(C.c_int32)), ("kv_len", C.POINTER(C.c_int32)),
+                ("kv_start", C.POINTER(C.c_int32)), ("n_heads", C.c_int32), ("n_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("causal", C.c_int32), ("scale", C.c_float), ("q", Heads),
+                ("k", Heads), ("v", Heads), ("o", Heads)]
+
+
+class LinearArgs(C.Structure):
+    _fields_ = [("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64), ("a", C.c_void_p), ("lda", C.c_int64),
+                ("w", C.c_void_p), ("ldw", C.c_int64), ("bias", C.c_void_p), ("act", C.c_int32),
+                ("residual", C.c_void_p), ("ld_residual", C.c_int64), ("residual_dtype", C.c_int32),
+                ("out", C.c_void_p), ("ld_out", C.c_int64), ("out_dtype", C.c_int32)]
+
+
 _SIGS = {
     "zdit_profile_begin": (C.c_int, [C.c_int32]),
     "zdit_profile_end": (C.c_int, [C.POINTER(ProfileEntry), C.c_int32, C.POINTER(C.c_int32)]),
@@ -106,6 +146,12 @@ _SIGS = {
                                      C.c_int32, C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p]),
     "zdit_gemm_bf16": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_int64,
                                  C.c_int64, C.c_void_p, C.c_void_p]),
+    "zdit_rope_table_scaled": (C.c_int, [C.c_void_p, C.c_int64, C.c_int32, C.c_float, C.POINTER(RopeScaling),
+                                         C.c_void_p, C.c_void_p, C.c_void_p]),
+    "zdit_qk_norm_rope": (C.c_int, [C.POINTER(QkNormRopeArgs), C.c_void_p]),
+    "zdit_prompt_attention_workspace_bytes": (C.c_size_t, [C.POINTER(PromptAttentionArgs)]),
+    "zdit_prompt_attention": (C.c_int, [C.POINTER(PromptAttentionArgs), C.c_void_p, C.c_size_t, C.c_void_p]),
+    "zdit_linear": (C.c_int, [C.POINTER(LinearArgs), C.c_void_p]),
     "zdit_patchify": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p]),
     "zdit_unpatchify": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p]),
     "zdit_device_status": (C.c_int, [C.c_void_p]),
@@ -304,6 +350,167 @@ def zdit_selftest_wait_timeout(result_dev, stream=None):
 
 def zdit_device_status(stream=None):
     return int(lib().zdit_device_status(_stream(stream)))
+
+
+# ------------------------------------------------------------------------ prompt operators
+# These take torch tensors of any strides the C calls allow.  What the C structs cannot
+# carry (element types, shapes, the device) is checked here.
+def _dtype_code(t, where):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return 0
+    if t.dtype == torch.float32:
+        return 1
+    raise ValueError(f"{where}: {t.dtype} is neither bfloat16 nor float32")
+
+
+def _on_device(where, *tensors):
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{where}: tensor on {t.device}, current device is cuda:{dev}")
+
+
+def _f32_vector(where, name, t, n):
+    import torch
+    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (n,) or not t.is_contiguous()):
+        raise ValueError(f"{where}: {name} must be a contiguous float32 [{n}]")
+
+
+def _heads(where, name, t, shape=None):
+    """Heads struct of a [rows, heads, head_dim] tensor whose last axis is contiguous."""
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {shape or '[rows, heads, head_dim]'}")
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError(f"{where}: {name}'s last axis must be contiguous")
+    return Heads(t.data_ptr(), st[0], st[1])
+
+
+def zdit_rope_table_scaled(pos, rotary_dim, theta, cos_out, sin_out, scaling: RopeScaling = None, stream=None):
+    """cos / sin [T, rotary_dim / 2] (fp32) of one int32 position per token."""
+    import torch
+    w = "zdit_rope_table_scaled"
+    T = pos.shape[0]
+    if pos.dtype != torch.int32 or pos.dim() != 1 or not pos.is_contiguous():
+        raise ValueError(f"{w}: pos must be a contiguous int32 vector")
+    for t in (cos_out, sin_out):
+        if t.dtype != torch.float32 or tuple(t.shape) != (T, rotary_dim // 2) or not t.is_contiguous():
+            raise ValueError(f"{w}: cos_out and sin_out must be contiguous float32 [{T}, {rotary_dim // 2}]")
+    _on_device(w, pos, cos_out, sin_out)
+    if T == 0:
+        return
+    _check(lib().zdit_rope_table_scaled(pos.data_ptr(), T, rotary_dim, theta,
+                                        C.byref(scaling) if scaling is not None else None, cos_out.data_ptr(),
+                                        sin_out.data_ptr(), _stream(stream)), w)
+
+
+def zdit_qk_norm_rope(q, k, q_out, k_out, w_q, w_k, cos, sin, rotary_dim, layout=ROPE_HALF, eps=1e-6, stream=None):
+    """Per-head RMSNorm (w_q / w_k fp32 [head_dim], None: no norm) and rotation of q [T, n_q,
+    head_dim] and k [T, n_k, head_dim] (k and k_out may be None) into q_out, k_out (which may
+    be q and k themselves)."""
+    import torch
+    w = "zdit_qk_norm_rope"
+    T, n_q, hd = q.shape
+    a = QkNormRopeArgs(T=T, n_q=n_q, n_k=0, head_dim=hd, in_dtype=_dtype_code(q, w), out_dtype=_dtype_code(q_out, w),
+                       eps=eps, rotary_dim=rotary_dim, layout=layout)
+    a.q, a.q_out = _heads(w, "q", q), _heads(w, "q_out", q_out, q.shape)
+    if (k is None) != (k_out is None):
+        raise ValueError(f"{w}: k and k_out go together")
+    if k is not None:
+        if k.dtype != q.dtype or k_out.dtype != q_out.dtype or k.shape[0] != T or k.shape[2] != hd:
+            raise ValueError(f"{w}: k must match q in type, rows and head_dim, k_out must match q_out in type")
+        a.n_k = k.shape[1]
+        a.k, a.k_out = _heads(w, "k", k), _heads(w, "k_out", k_out, k.shape)
+    _f32_vector(w, "w_q", w_q, hd)
+    _f32_vector(w, "w_k", w_k, hd)
+    if rotary_dim:
+        for t in (cos, sin):
+            if t is None or t.dtype != torch.float32 or tuple(t.shape) != (T, rotary_dim // 2) or not t.is_contiguous():
+                raise ValueError(f"{w}: cos and sin must be contiguous float32 [{T}, {rotary_dim // 2}]")
+        a.cos, a.sin = cos.data_ptr(), sin.data_ptr()
+    _on_device(w, q, k, q_out, k_out, w_q, w_k, cos, sin)
+    if T == 0:
+        return
+    a.w_q = w_q.data_ptr() if w_q is not None else None
+    a.w_k = w_k.data_ptr() if w_k is not None else None
+    _check(lib().zdit_qk_norm_rope(C.byref(a), _stream(stream)), w)
+
+
+class PromptBatch:
+    """Lengths of the packed sequences of zdit_prompt_attention (host arrays, kept alive):
+    q_len new rows each; kv_len keys each (None: q_len); kv_start first key row of each
+    (None: packed one after the other)."""
+
+    def __init__(self, q_len, kv_len=None, kv_start=None):
+        arr = lambda v: None if v is None else (C.c_int32 * len(v))(*[int(x) for x in v])
+        n = len(q_len)
+        if any(v is not None and len(v) != n for v in (kv_len, kv_start)):
+            raise ValueError("PromptBatch: q_len, kv_len and kv_start must have one entry per sequence")
+        self.batch = n
+        self.q_len, self.kv_len, self.kv_start = arr(q_len), arr(kv_len), arr(kv_start)
+        self.q_rows = sum(self.q_len)
+        lens = list(self.q_len if kv_len is None else self.kv_len)
+        ends = [s + m for s, m in zip(self.kv_start, lens)] if kv_start is not None else [sum(lens)]
+        self.kv_rows = max(ends) if ends else 0
+
+    def args(self, n_heads, n_kv_heads, head_dim, causal, scale):
+        return PromptAttentionArgs(batch=self.batch, q_len=self.q_len, kv_len=self.kv_len, kv_start=self.kv_start,
+                                   n_heads=n_heads, n_kv_heads=n_kv_heads, head_dim=head_dim,
+                                   causal=1 if causal else 0, scale=scale)
+
+
+def prompt_attention_workspace_bytes(batch: PromptBatch, n_heads, n_kv_heads, head_dim, causal=True) -> int:
+    a = batch.args(n_heads, n_kv_heads, head_dim, causal, 0.0)
+    return int(lib().zdit_prompt_attention_workspace_bytes(C.byref(a)))
+
+
+def zdit_prompt_attention(q, k, v, o, batch: PromptBatch, workspace=None, causal=True, scale=0.0, stream=None):
+    """Attention of packed prompts: q, o [rows, n_heads, head_dim], k, v [rows, n_kv_heads,
+    head_dim], bf16, any row and head strides.  workspace: a uint8 tensor of
+    prompt_attention_workspace_bytes (None when that is 0)."""
+    import torch
+    w = "zdit_prompt_attention"
+    if any(t.dtype != torch.bfloat16 for t in (q, k, v, o)):
+        raise ValueError(f"{w}: q, k, v and o must be bfloat16")
+    a = batch.args(q.shape[1], k.shape[1], q.shape[2], causal, scale)
+    a.q, a.k, a.v, a.o = _heads(w, "q", q), _heads(w, "k", k), _heads(w, "v", v, k.shape), _heads(w, "o", o)
+    if o.shape[1:] != q.shape[1:] or k.shape[2] != q.shape[2]:
+        raise ValueError(f"{w}: o must match q and k must match q's head_dim")
+    if q.shape[0] < batch.q_rows or o.shape[0] < batch.q_rows or k.shape[0] < batch.kv_rows:
+        raise ValueError(f"{w}: the batch needs {batch.q_rows} rows of q and o and {batch.kv_rows} of k and v")
+    _on_device(w, q, k, v, o, workspace)
+    _check(lib().zdit_prompt_attention(C.byref(a), _ptr(workspace),
+                                       workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                       _stream(stream)), w)
+
+
+def zdit_linear(a, w, out, bias=None, act=ACT_NONE, residual=None, stream=None):
+    """out [M, N] = residual + act(a [M, K] . w [N, K]^T + bias): a and w bf16, bias fp32,
+    residual and out fp32 or bf16; residual may be out."""
+    import torch
+    n = "zdit_linear"
+    M, K = a.shape
+    N = w.shape[0]
+    if a.dtype != torch.bfloat16 or w.dtype != torch.bfloat16 or w.dim() != 2 or w.shape[1] != K:
+        raise ValueError(f"{n}: a [M, K] and w [N, K] must be bfloat16 matrices with the same K")
+    for t in (out, residual):
+        if t is not None and (tuple(t.shape) != (M, N) or (N > 1 and t.stride(1) != 1)):
+            raise ValueError(f"{n}: out and residual must be [{M}, {N}] with contiguous rows")
+    if K > 1 and (a.stride(1) != 1 or w.stride(1) != 1):
+        raise ValueError(f"{n}: rows of a and w must be contiguous")
+    _f32_vector(n, "bias", bias, N)
+    out_dtype, res_dtype = _dtype_code(out, n), 0 if residual is None else _dtype_code(residual, n)
+    _on_device(n, a, w, out, bias, residual)
+    if M == 0:
+        return
+    g = LinearArgs(M=M, N=N, K=K, a=a.data_ptr(), lda=a.stride(0), w=w.data_ptr(), ldw=w.stride(0),
+                   bias=bias.data_ptr() if bias is not None else None, act=act, out=out.data_ptr(),
+                   ld_out=out.stride(0), out_dtype=out_dtype)
+    if residual is not None:
+        g.residual, g.ld_residual, g.residual_dtype = residual.data_ptr(), residual.stride(0), res_dtype
+    _check(lib().zdit_linear(C.byref(g), _stream(stream)), n)
 
 
 # ------------------------------------------------------------------------ stack

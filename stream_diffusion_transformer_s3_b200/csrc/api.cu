@@ -44,17 +44,17 @@ int num_sms() {
   return n;
 }
 
-namespace {
-
-constexpr int kMaxBatch = 8;
-constexpr int kMaxBlocks = 256;
-
 // the current device is a compute capability 10.x part (checked per call, like num_sms)
 bool device_ok() {
   int dev = 0, major = 0;
   return cudaGetDevice(&dev) == cudaSuccess &&
          cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) == cudaSuccess && major == 10;
 }
+
+namespace {
+
+constexpr int kMaxBatch = 8;
+constexpr int kMaxBlocks = 256;
 
 size_t align_up(size_t v, size_t a = 256) { return (v + a - 1) / a * a; }
 

@@ -20,6 +20,7 @@
 //              chunks; bf16 store of [q | k | v]
 //   EPI_QKV_NORM  same with a per-head RMSNorm of q and k first (whole head at once)
 //   EPI_SWIGLU gate/up column blocks -> silu(gate) * up, bf16 store
+//   EPI_LINEAR residual + act(acc + bias), bf16 or fp32, ragged columns   zdit_linear
 #include <cudaTypedefs.h>
 
 #include <cstdio>
@@ -27,6 +28,7 @@
 #include <mutex>
 
 #include "internal.h"
+#include "linear_epi.cuh"
 #include "ptx.cuh"
 
 #ifndef ZDIT_L2_BAND_MB
@@ -58,6 +60,7 @@ struct KParams {
   int num_m, num_n, num_k, group_m, group_n, raster;
   int* err;
   int* band_flags;  // per 128-row band arrival counters or nullptr
+  LinearEpi lin;    // EPI_LINEAR only
 };
 
 // Tile order of the persistent loop.  raster 0: bands of group_m M-tiles, M fastest
@@ -122,6 +125,21 @@ __device__ __forceinline__ void epilogue_tile(const KParams& p, uint32_t taddr, 
                                 pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
         }
       }
+    }
+  } else if constexpr (EPI == EPI_LINEAR) {
+#pragma unroll 1
+    for (int c = 0; c < BN / 32; ++c) {
+      const int col0 = nb * BN + c * 32;
+      if (col0 >= p.N) break;  // warp-uniform
+      uint32_t r[32];
+      __syncwarp();
+      tmem_ld32(taddr + c * 32, r);
+      tmem_ld_wait();
+      if (!row_ok) continue;
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+      linear_finish_row<32>(p.lin, row, col0, p.N, v);
     }
   } else if constexpr (EPI == EPI_SWIGLU) {
     // tile columns [0,128) hold gate rows 128*nb.., [128,256) the matching up rows
@@ -616,6 +634,23 @@ bool make_tmap_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t 
   return r == CUDA_SUCCESS;
 }
 
+// Rows of heads: element (d, head, row) at ptr + (row * row_stride + head * head_stride + d)
+// elements; a box of 64 columns x box_heads x box_rows lands as box_heads * box_rows
+// consecutive 128-byte rows (row-major over rows, heads inside), 128-byte swizzled.
+bool make_tmap_bf16_heads(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t heads, uint64_t head_dim,
+                          uint64_t row_stride, uint64_t head_stride, uint32_t box_heads, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {head_dim, heads, rows};
+  cuuint64_t strides[2] = {(heads > 1 ? head_stride : head_dim) * 2, (rows > 1 ? row_stride : head_dim) * 2};
+  cuuint32_t box[3] = {64, box_heads, box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // ZDIT_GEMM_SINGLE_CTA=1 in the environment selects the single-CTA kernel for every
 // shape (A/B comparisons of the two kernels).
 bool force_single_cta() {
@@ -631,9 +666,12 @@ bool gemm_uses_pair(int M, int N) { return M > 256 && N % BN == 0 && !force_sing
 
 zdit_status launch_gemm(const GemmArgs& a, cudaStream_t s) {
   if (a.M <= 0 || a.N <= 0 || a.K <= 0) return ZDIT_ERR_SHAPE;
-  if (a.K % 8 || a.lda % 8 || a.ldb % 8 || a.N % 32) return ZDIT_ERR_SHAPE;
+  // EPI_LINEAR takes any N and K: columns past them are zero-filled by the tensor maps and
+  // left out by the epilogue, which also takes any element alignment of the output
+  const bool linear = a.epi == EPI_LINEAR;
+  if (a.lda % 8 || a.ldb % 8 || (!linear && (a.K % 8 || a.N % 32))) return ZDIT_ERR_SHAPE;
   if ((reinterpret_cast<uintptr_t>(a.A) | reinterpret_cast<uintptr_t>(a.B) |
-       reinterpret_cast<uintptr_t>(a.out)) & 15)
+       (linear ? 0 : reinterpret_cast<uintptr_t>(a.out))) & 15)
     return ZDIT_ERR_ALIGNMENT;
   if (a.epi == EPI_SWIGLU && (a.N % BN)) return ZDIT_ERR_SHAPE;
   if (a.epi == EPI_QKV && (a.N != 3 * a.dim || a.dim % 128 || a.N % BN || !a.rope_cos || !a.rope_sin))
@@ -641,7 +679,7 @@ zdit_status launch_gemm(const GemmArgs& a, cudaStream_t s) {
   if ((a.epi == EPI_F32 || a.epi == EPI_BF16) && (a.ldo % 4)) return ZDIT_ERR_ALIGNMENT;
   // CTA pairs for every shape that fills several 256 x 256 tiles; the single-CTA
   // kernel for small or narrow problems (embedders, final layer, tiny blocks).
-  const bool pair = a.M > 256 && a.N % BN == 0 && !force_single_cta();
+  const bool pair = a.M > 256 && (linear || a.N % BN == 0) && !force_single_cta();
   CUtensorMap ta, tb;
   if (!make_tmap_bf16_2d(&ta, a.A, a.M, a.K, a.lda, BM, BK)) return ZDIT_ERR_CUDA;
   if (!make_tmap_bf16_2d(&tb, a.B, a.N, a.K, a.ldb, pair ? 128 : BN, BK)) return ZDIT_ERR_CUDA;
@@ -670,13 +708,15 @@ zdit_status launch_gemm(const GemmArgs& a, cudaStream_t s) {
   }
   kp.err = device_error_ptr();
   kp.band_flags = pair ? a.band_flags : nullptr;
+  kp.lin = a.lin;
   const int tiles = kp.num_m * kp.num_n;
   int grid = tiles < num_sms() ? tiles : num_sms();
   if (pair) {
     const int pairs = num_sms() / 2;
     grid = 2 * (tiles < pairs ? tiles : pairs);
   }
-  const double out_elt = (a.epi == EPI_F32) ? 4.0 : 2.0;
+  const double out_elt = linear ? (a.lin.out_f32 ? 4.0 : 2.0) + (a.lin.residual ? (a.lin.res_f32 ? 4.0 : 2.0) : 0.0)
+                                : (a.epi == EPI_F32) ? 4.0 : 2.0;
   const double out_cols = (a.epi == EPI_SWIGLU) ? a.N / 2.0 : (double)a.N;
   ProfScope ps(a.prof_kind, 2.0 * a.M * a.N * (double)a.K,
                2.0 * ((double)a.M * a.K + (double)a.N * a.K) + out_elt * a.M * out_cols, s);
@@ -687,6 +727,7 @@ zdit_status launch_gemm(const GemmArgs& a, cudaStream_t s) {
       return a.qn != nullptr ? launch_epi<EPI_QKV_NORM>(ta, tb, kp, grid, pair, s)
                              : launch_epi<EPI_QKV>(ta, tb, kp, grid, pair, s);
     case EPI_SWIGLU: return launch_epi<EPI_SWIGLU>(ta, tb, kp, grid, pair, s);
+    case EPI_LINEAR: return launch_epi<EPI_LINEAR>(ta, tb, kp, grid, pair, s);
   }
   return ZDIT_ERR_INVALID_ARG;
 }

@@ -42,6 +42,18 @@ enum GemmEpilogue : int {
   EPI_QKV = 2,     // out bf16 [M, 3D]; columns < 2D: optional per-head RMSNorm, then RoPE
   EPI_SWIGLU = 3,  // out bf16 [M, N/2]; tile columns [gate 128 | up 128] -> silu(g) * u
   EPI_QKV_NORM = 4,  // EPI_QKV with per-head RMSNorm of q and k before RoPE (selected when qn != null)
+  EPI_LINEAR = 5,    // out = residual + act(acc + bias), any N and element alignment (see LinearEpi)
+};
+
+// Epilogue of zdit_linear (EPI_LINEAR and the few-row kernel of linear.cu).
+struct LinearEpi {
+  const float* bias;     // [N] or nullptr
+  const void* residual;  // [M, ld_res] fp32 or bf16, or nullptr
+  void* out;             // [M, ld_out] fp32 or bf16
+  int64_t ld_res, ld_out;
+  int act;               // ZDIT_ACT_*
+  int res_f32, out_f32;
+  int vec;               // 1: rows of out (and residual) start 16-byte aligned, ld alike
 };
 
 struct GemmArgs {
@@ -64,6 +76,7 @@ struct GemmArgs {
   // per launch), so a row consumer can start on a band before the whole GEMM ends.
   // Only honoured on the pair path (gemm_uses_pair).
   int* band_flags = nullptr;
+  LinearEpi lin{};        // EPI_LINEAR
 };
 
 zdit_status launch_gemm(const GemmArgs& a, cudaStream_t s);
@@ -130,6 +143,8 @@ zdit_status check_block_call(const zdit_block_cfg* cfg, const zdit_block_weights
                              const void* workspace, bool with_workspace);
 
 int num_sms();
+// the current device is one this library is built for
+bool device_ok();
 // true while zdit_profile_begin .. zdit_profile_end is recording
 bool profiling_on();
 // adds n to the launch counter (kernels replayed from a captured graph)

@@ -1,0 +1,771 @@
+// Causal attention with grouped heads over packed prompts, for sm_100a (head dim 64 or 128).
+//
+//   O_i = sum_j p_ij V_j,  p_i = softmax_j(scale q_i . k_j),  j <= i + kv_len - q_len
+//
+// The `group` query heads that share a key head are packed into one 128-row tile: a tile
+// holds 128 / group consecutive tokens, row r = (token r / group, head r % group), which a
+// 3-D TMA box (64 columns x group heads x tokens) delivers as consecutive rows.  So K and V
+// are read once per key head, a single token fills `group` rows instead of one, and the mask
+// is a limit on the key index that depends on the row's token alone.
+//
+// One CTA = one item (sequence, key head, rows, range of 128-key tiles) with two softmax
+// slots of 128 threads, one thread per row:
+//   two query tiles  slots 0 and 1 take consecutive query tiles and the same key tiles
+//                    (arithmetic-bound: each K and V tile feeds 256 rows);
+//   one query tile   slots 0 and 1 take even and odd key tiles of the same rows and are
+//                    joined in shared memory (few rows: memory- and latency-bound, the
+//                    tensor core and softmax of one slot overlap the other's).
+// Warp roles (384 threads): warps 0-3 and 4-7 softmax of slots 0 and 1, warp 8 loads Q and
+// K, warp 9 issues the MMAs, warp 10 loads V (its own warp, so that a V stage still in use
+// never delays the next K), warp 11 completes the warpgroup that hands registers over
+// (168 per thread at launch -> 208 softmax, 88 control: 2 x 128 x 208 + 128 x 88 = 64512).
+// TMEM columns: S0 [0,128), S1 [128,256), O0 [256, +HD), O1 [384, +HD).  P (bf16 pairs) is
+// written over the first 64 columns of S and feeds the PV product from TMEM.
+// A slot's PV of its previous key tile is issued before its next S product, so the commit
+// that signals the new S also proves that PV done: the softmax may overwrite P and rescale O.
+// Softmax in fp32: running maximum that moves only when a row grows by more than 16 (log2
+// units; P <= 2^16 keeps bf16's relative precision), sum of the unrounded P in fp32.
+//
+// Keys are split when the items would not fill the GPU: each part writes its normalised O
+// (fp32) with its maximum and sum to the workspace and a second kernel joins the parts of
+// a row in ascending order.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace zdit {
+
+bool make_tmap_bf16_heads(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t heads, uint64_t head_dim,
+                          uint64_t row_stride, uint64_t head_stride, uint32_t box_heads, uint32_t box_rows);
+bool heads_disjoint(const zdit_heads& h, int64_t rows, int heads, int head_dim);
+
+namespace {
+
+constexpr int TILE = 128;  // rows of a query tile, keys of a key tile
+constexpr int THREADS = 384;
+constexpr int WARP_QK = 8, WARP_MMA = 9, WARP_V = 10;
+constexpr int kMaxSeqs = 128;
+constexpr float kRescaleThreshold = 16.0f;  // log2 units
+
+// Per-sequence plan, in the order the items are launched (longest key range first).
+struct Plan {
+  int n;  // sequences with query rows
+  int item0[kMaxSeqs + 1];  // first item (per key head) of sequence i; item0[n] = all
+  int q0[kMaxSeqs], q_len[kMaxSeqs], kv0[kMaxSeqs], kv_len[kMaxSeqs];
+  int parts[kMaxSeqs];      // key splits
+  int part0[kMaxSeqs];      // first partial row of the sequence in the workspace (parts > 1)
+  int join0[kMaxSeqs + 1];  // first joined row (token, head) among sequences with parts > 1
+};
+
+struct PParams {
+  int n_kv, group, tokens;  // tokens per query tile
+  int chunk;                // key tiles per part
+  int causal;
+  float scale_log2;
+  __nv_bfloat16* o;
+  int64_t o_rs, o_hs;
+  float* part_o;    // [rows][HD] normalised partial outputs
+  float2* part_ml;  // [rows] (maximum in log2 units, sum)
+  int* err;
+};
+
+template <int HD>
+struct Cfg {
+  static constexpr int HALF = TILE * 128;               // 64 columns x 128 rows, 16 KB
+  static constexpr int TILE_BYTES = (HD / 64) * HALF;
+  static constexpr int ST = HD == 128 ? 2 : 4;          // K and V ring depth (64 KB each)
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = 2 * TILE_BYTES;
+  static constexpr int OFF_V = OFF_K + ST * TILE_BYTES;
+  static constexpr int OFF_BAR = OFF_V + ST * TILE_BYTES;
+  static constexpr int SMEM = 1024 + OFF_BAR + 256;
+  static constexpr int STAGE_ROW = 2 * HD + 16;         // bf16 output row, padded against bank conflicts
+  static constexpr int JOIN_ROW = HD + 4;               // fp32 row of slot 1 when slots are joined
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpk2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Largest key index allowed for query token `tok` of a sequence (-1: none).
+__device__ __forceinline__ int last_key(int tok, int q_len, int kv_len, int causal) {
+  return causal ? min(tok + kv_len - q_len, kv_len - 1) : kv_len - 1;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(THREADS, 1)
+    prompt_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Plan plan, const PParams p) {
+  using C = Cfg<HD>;
+  constexpr int ST = C::ST;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_full = bars;              // [2]
+  uint64_t* s_full = bars + 2;          // [2]
+  uint64_t* p_full = bars + 4;          // [2]
+  uint64_t* o_full = bars + 6;          // [2]
+  uint64_t* mma_done = bars + 8;
+  uint64_t* k_full = bars + 9;          // [ST]
+  uint64_t* k_empty = k_full + ST;      // [ST]
+  uint64_t* v_full = k_empty + ST;      // [ST]
+  uint64_t* v_empty = v_full + ST;      // [ST]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_empty + ST);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  griddep_wait();     // Q, K, V of the predecessor are complete, the workspace is free
+  griddep_trigger();  // every CTA has started: the successor may launch
+
+  // item of this CTA: key heads fastest, so that all heavy items come first
+  const int item = blockIdx.x / p.n_kv;
+  const int kvh = blockIdx.x - item * p.n_kv;
+  int lo = 0, hi = plan.n;  // plan.item0[lo] <= item < plan.item0[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (plan.item0[mid] <= item) lo = mid; else hi = mid;
+  }
+  const int sq = lo;
+  const int q_len = plan.q_len[sq], kv_len = plan.kv_len[sq], kv0 = plan.kv0[sq], q0 = plan.q0[sq];
+  const int parts = plan.parts[sq];
+  const int rem = item - plan.item0[sq];
+  const int n_pairs = (q_len + 2 * p.tokens - 1) / (2 * p.tokens);
+  const int part = rem % parts;
+  const int pair = n_pairs - 1 - rem / parts;  // later rows see more keys: first
+  const int tok0 = pair * 2 * p.tokens;
+  const bool two = tok0 + p.tokens < q_len;    // two query tiles, or one with split keys
+  const int first_tile = part * p.chunk;
+  // key tiles [first_tile, first_tile + n) of this item; slot 0 of two stops after n0
+  auto tiles_for = [&](int tok_end) {
+    const int lk = last_key(min(tok_end, q_len) - 1, q_len, kv_len, p.causal);
+    int t = lk < 0 ? 0 : lk / TILE + 1;
+    if (parts > 1) t = min(t, first_tile + p.chunk);
+    return max(t - first_tile, 0);
+  };
+  const int n0 = tiles_for(tok0 + p.tokens);
+  const int n = two ? tiles_for(tok0 + 2 * p.tokens) : n0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+    }
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == WARP_QK && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+  }
+  if (warp == WARP_V && lane == 0) tma_prefetch_desc(&tmV);
+  if (warp == WARP_MMA) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::: "memory");
+    if (warp == WARP_QK && lane == 0 && n > 0) {
+      // ------------------------------------------------------------ Q and K
+      const uint32_t q_bytes = (uint32_t)(p.group * p.tokens * 128 * (HD / 64));
+      auto load_q = [&](int t) {
+        uint8_t* sQ = smem + C::OFF_Q + t * C::TILE_BYTES;
+        mbar_arrive_expect_tx(&q_full[t], q_bytes);
+        for (int c = 0; c < HD / 64; ++c)
+          tma_load_3d(sQ + c * C::HALF, &tmQ, &q_full[t], c * 64, kvh * p.group, q0 + tok0 + t * p.tokens);
+      };
+      load_q(0);
+      int issued = 0;
+      for (int i = 0; i < n; ++i) {
+        const int st = i % ST;
+        if (!mbar_wait(&k_empty[st], ((i / ST) & 1) ^ 1, abort_flag, p.err)) break;
+        uint8_t* sK = smem + C::OFF_K + st * C::TILE_BYTES;
+        mbar_arrive_expect_tx(&k_full[st], C::TILE_BYTES);
+        for (int c = 0; c < HD / 64; ++c)
+          tma_load_3d(sK + c * C::HALF, &tmK, &k_full[st], c * 64, kvh, kv0 + (first_tile + i) * TILE);
+        ++issued;
+        if (i == 0 && two) load_q(1);
+      }
+      if (*abort_flag) {  // let copies in flight land before shared memory is released
+        int dummy = 0;
+        mbar_wait(&q_full[0], 0, &dummy);
+        if (two && issued > 0) mbar_wait(&q_full[1], 0, &dummy);
+        for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(&k_full[i % ST], (i / ST) & 1, &dummy);
+      }
+    } else if (warp == WARP_V && lane == 0) {
+      // ------------------------------------------------------------ V
+      int issued = 0;
+      for (int i = 0; i < n; ++i) {
+        const int st = i % ST;
+        if (!mbar_wait(&v_empty[st], ((i / ST) & 1) ^ 1, abort_flag, p.err)) break;
+        uint8_t* sV = smem + C::OFF_V + st * C::TILE_BYTES;
+        mbar_arrive_expect_tx(&v_full[st], C::TILE_BYTES);
+        for (int c = 0; c < HD / 64; ++c)
+          tma_load_3d(sV + c * C::HALF, &tmV, &v_full[st], c * 64, kvh, kv0 + (first_tile + i) * TILE);
+        ++issued;
+      }
+      if (*abort_flag) {
+        int dummy = 0;
+        for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(&v_full[i % ST], (i / ST) & 1, &dummy);
+      }
+    } else if (warp == WARP_MMA && lane == 0 && n > 0) {
+      // ------------------------------------------------------------ MMA issuer
+      const uint32_t id_s = idesc_bf16_f32(TILE, TILE);             // Q, K both K-major
+      const uint32_t id_o = idesc_bf16_f32(TILE, HD, false, true);  // P from TMEM, V MN-major
+      const uint64_t dq = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_Q));
+      const uint64_t dk = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_K));
+      const uint64_t dv = sdesc_mnmajor_sw128(smem_u32(smem + C::OFF_V), C::HALF, 1024);
+      constexpr uint64_t kTileDesc = C::TILE_BYTES >> 4;  // descriptors are linear in the address
+      auto koff = [](int k) -> uint64_t { return (uint64_t)(((k >> 2) * C::HALF + (k & 3) * 32) >> 4); };
+      auto voff = [](int k) -> uint64_t { return (uint64_t)((k * 16 * 128) >> 4); };
+      // O_t (+)= P_t V_i, the c-th product of slot t
+      auto pv = [&](int t, int i, int c) -> bool {
+        if (!mbar_wait(&p_full[t], c & 1, abort_flag, p.err)) return false;
+        if (!mbar_wait(&v_full[i % ST], (i / ST) & 1, abort_flag, p.err)) return false;
+        tc_fence_after();
+        const uint64_t vb = dv + (i % ST) * kTileDesc;
+        const uint32_t d = tmem + 256 + t * 128, pa = tmem + t * 128;
+        umma_bf16_ts(d, pa, vb, id_o, c != 0 ? 1u : 0u);
+#pragma unroll
+        for (int k = 1; k < TILE / 16; ++k) umma_bf16_ts(d, pa + k * 8, vb + voff(k), id_o, 1u);
+        return true;
+      };
+      // S_t = Q_qt K_i^T
+      auto sk = [&](int t, int qt, int i) {
+        const uint64_t kb = dk + (i % ST) * kTileDesc, qb = dq + qt * kTileDesc;
+        const uint32_t d = tmem + t * 128;
+        umma_bf16_ss(d, qb, kb, id_s, 0u);
+#pragma unroll
+        for (int k = 1; k < HD / 16; ++k) umma_bf16_ss(d, qb + koff(k), kb + koff(k), id_s, 1u);
+        umma_commit(&s_full[t]);
+      };
+      bool ok = mbar_wait(&q_full[0], 0, abort_flag, p.err);
+      if (two) {
+        for (int i = 0; ok && i < n; ++i) {
+          if (!(ok = mbar_wait(&k_full[i % ST], (i / ST) & 1, abort_flag, p.err))) break;
+          tc_fence_after();
+          if (i > 0 && i <= n0 && !(ok = pv(0, i - 1, i - 1))) break;
+          if (i < n0) sk(0, 0, i);
+          if (i > 0) {
+            if (!(ok = pv(1, i - 1, i - 1))) break;
+            umma_commit(&v_empty[(i - 1) % ST]);
+          }
+          if (i == 0 && !(ok = mbar_wait(&q_full[1], 0, abort_flag, p.err))) break;
+          sk(1, 1, i);
+          umma_commit(&k_empty[i % ST]);
+        }
+        if (ok && n0 == n) ok = pv(0, n - 1, n - 1);
+        if (ok) umma_commit(&o_full[0]);  // after every S product: Q and K are idle
+        if (ok && pv(1, n - 1, n - 1)) umma_commit(&o_full[1]);
+      } else {
+        for (int i = 0; ok && i < n; ++i) {
+          if (!(ok = mbar_wait(&k_full[i % ST], (i / ST) & 1, abort_flag, p.err))) break;
+          tc_fence_after();
+          const int t = i & 1;
+          if (i > 1) {
+            if (!(ok = pv(t, i - 2, (i >> 1) - 1))) break;
+            umma_commit(&v_empty[(i - 2) % ST]);
+          }
+          sk(t, 0, i);
+          umma_commit(&k_empty[i % ST]);
+        }
+        if (ok && n > 1 && (ok = pv(n & 1, n - 2, (n - 2) >> 1))) umma_commit(&o_full[n & 1]);
+        if (ok && pv((n - 1) & 1, n - 1, (n - 1) >> 1)) umma_commit(&o_full[(n - 1) & 1]);
+      }
+      umma_commit(mma_done);
+      int dummy = 0;
+      mbar_wait(mma_done, 0, &dummy);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n" ::: "memory");
+    // ------------------------------------------------------------ softmax
+    const int t = warp >> 2;   // slot
+    const int lg = warp & 3;   // TMEM lane group
+    const int row = lg * 32 + lane;
+    const int tok = tok0 + (two ? t * p.tokens : 0) + row / p.group;
+    const int head = kvh * p.group + row % p.group;
+    const bool live = row < p.group * p.tokens && tok < q_len;
+    const bool warp_live = __any_sync(0xffffffffu, live);
+    const int lim = live ? last_key(tok, q_len, kv_len, p.causal) : kv_len - 1;
+    const uint32_t lane_off = (uint32_t)(lg * 32) << 16;
+    const uint32_t tS = tmem + lane_off + t * 128;
+    const uint32_t tO = tmem + lane_off + 256 + t * 128;
+    const int cnt = two ? (t == 0 ? n0 : n) : (n + 1 - t) >> 1;
+    float m_ref = -INFINITY, l_sum = 0.f;
+    bool ok = true;
+    for (int c = 0; c < cnt; ++c) {
+      const int i = two ? c : 2 * c + t;
+      const int key0 = (first_tile + i) * TILE;
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], c & 1, abort_flag, p.err));
+      if (!ok) break;
+      tc_fence_after();
+      if (key0 + TILE > kv_len && (!two || t == 0 || i >= n0)) {
+        // keys past the end of the sequence: their P is 0, but 0 times whatever the rows of
+        // V there hold need not be, so the rows are cleared (by the slot that uses them first)
+        ok = __all_sync(0xffffffffu, mbar_wait(&v_full[i % ST], (i / ST) & 1, abort_flag, p.err));
+        if (!ok) break;
+        if (row >= kv_len - key0) {
+          uint8_t* sV = smem + C::OFF_V + (i % ST) * C::TILE_BYTES + row * 128;
+          for (int h = 0; h < HD / 64; ++h)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(sV + h * C::HALF + e * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      if (warp_live) {
+        float s[TILE];
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+          uint32_t r[32];
+          tmem_ld32(tS + e4 * 32, r);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) s[e4 * 32 + e] = __uint_as_float(r[e]);
+        }
+        tmem_ld_wait();
+        const int valid = lim - key0;  // last allowed column of this tile
+        if (valid < TILE - 1) {
+#pragma unroll
+          for (int e = 0; e < TILE; ++e)
+            if (e > valid) s[e] = -INFINITY;
+        }
+        // row max: 8 independent chains of 3-input max
+        float m8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m8[e] = fmaxf(s[e], s[8 + e]);
+#pragma unroll
+        for (int e = 16; e < TILE; e += 16)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) m8[k] = fmax3(m8[k], s[e + k], s[e + 8 + k]);
+        float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], fmax3(m8[5], m8[6], m8[7])));
+        mx *= p.scale_log2;
+        float alpha = 1.f;
+        bool move = false;
+        if (c == 0) {
+          m_ref = mx;
+        } else if (mx > m_ref + kRescaleThreshold) {
+          alpha = ex2(m_ref - mx);
+          m_ref = mx;
+          move = true;
+        }
+        l_sum *= alpha;
+        if (__any_sync(0xffffffffu, move)) {  // O is stable: the previous PV completed before this S
+#pragma unroll 1
+          for (int e = 0; e < HD / 16; ++e) {
+            uint32_t r[16];
+            tmem_ld16(tO + e * 16, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha);
+            tmem_st16(tO + e * 16, r);
+          }
+        }
+        // P = exp2(s scale - m_ref); a row with no key yet has m_ref = -inf: use 0, P = 0
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        const uint64_t sc2 = pk2(p.scale_log2, p.scale_log2);
+        const uint64_t nm2 = pk2(-m_use, -m_use);
+        uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const uint64_t x2 = fma2(pk2(s[e4 * 32 + 2 * e], s[e4 * 32 + 2 * e + 1]), sc2, nm2);
+            float a, b;
+            unpk2(x2, a, b);
+            const float p0 = ex2(a), p1 = ex2(b);
+            sum4[e & 3] = add2(sum4[e & 3], pk2(p0, p1));
+            pk[e] = pack_bf16x2(p0, p1);
+          }
+          tmem_st16(tS + e4 * 16, pk);
+        }
+        float a0, a1, a2, a3, a4, a5, a6, a7;
+        unpk2(sum4[0], a0, a1);
+        unpk2(sum4[1], a2, a3);
+        unpk2(sum4[2], a4, a5);
+        unpk2(sum4[3], a6, a7);
+        l_sum += ((a0 + a1) + (a2 + a3)) + ((a4 + a5) + (a6 + a7));
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[t]);
+    }
+    // ------------------------------------------------------------ epilogue
+    // Both slots' products are awaited before shared memory is reused for staging.
+    if (ok && (cnt > 0 || (two && n > 0)))
+      ok = __all_sync(0xffffffffu, mbar_wait(&o_full[t], 0, abort_flag, p.err));
+    tc_fence_after();
+    float wa = 1.f, wb = 0.f;  // weights of this slot's O and of slot 1's when joined
+    float* join = reinterpret_cast<float*>(smem + C::OFF_V / 2);
+    float2* join_ml = reinterpret_cast<float2*>(smem + C::OFF_V / 2 + TILE * C::JOIN_ROW * 4);
+    if (!two && n > 1) {
+      if (t == 1) {
+        // slot 0's last S product may still read K here: wait for everything
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&o_full[0], 0, abort_flag, p.err));
+        if (ok && warp_live) {
+          for (int e4 = 0; e4 < HD / 32; ++e4) {
+            uint32_t r[32];
+            tmem_ld32(tO + e4 * 32, r);
+            tmem_ld_wait();
+            float4* dst = reinterpret_cast<float4*>(join + row * C::JOIN_ROW + e4 * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
+                                   __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
+          }
+          join_ml[row] = make_float2(m_ref, l_sum);
+        }
+      }
+      named_bar_sync(1, 256);
+      if (t == 0) {
+        const float2 b = join_ml[row];
+        const float m = fmaxf(m_ref, b.x), mu = m == -INFINITY ? 0.f : m;
+        wa = ex2(m_ref - mu);
+        wb = ex2(b.x - mu);
+        l_sum = l_sum * wa + b.y * wb;
+        m_ref = m;
+      }
+    }
+    if (ok && (two || t == 0)) {
+      const float inv = l_sum == 0.f ? 0.f : 1.0f / l_sum;
+      wa *= inv;
+      wb *= inv;
+      const bool joined = !two && n > 1;
+      auto take = [&](int e4, float (&v)[32]) {  // 32 columns of the finished row
+        if (cnt > 0) {
+          uint32_t r[32];
+          tmem_ld32(tO + e4 * 32, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]) * wa;
+          if (joined) {
+            const float4* src = reinterpret_cast<const float4*>(join + row * C::JOIN_ROW + e4 * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 q = src[e];
+              v[4 * e] = fmaf(q.x, wb, v[4 * e]);
+              v[4 * e + 1] = fmaf(q.y, wb, v[4 * e + 1]);
+              v[4 * e + 2] = fmaf(q.z, wb, v[4 * e + 2]);
+              v[4 * e + 3] = fmaf(q.w, wb, v[4 * e + 3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0.f;
+        }
+      };
+      if (parts > 1) {
+        if (warp_live) {
+          const int64_t at = (int64_t)plan.part0[sq] +
+                             ((int64_t)part * q_len + tok) * (p.n_kv * p.group) + head;
+          if (live) p.part_ml[at] = make_float2(m_ref, l_sum);
+          for (int e4 = 0; e4 < HD / 32; ++e4) {
+            float v[32];
+            take(e4, v);
+            if (live) {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + e4 * 32);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
+            __syncwarp();
+          }
+        }
+      } else if (warp_live) {
+        // bf16 rows staged in the idle Q and K space of this slot, stored as whole rows
+        uint8_t* stage = smem + C::OFF_Q + t * (C::OFF_V / 2) + lg * 32 * C::STAGE_ROW;
+        for (int e4 = 0; e4 < HD / 32; ++e4) {
+          float v[32];
+          take(e4, v);
+          uint4* dst = reinterpret_cast<uint4*>(stage + lane * C::STAGE_ROW + e4 * 64);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                                pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+        }
+        __syncwarp();
+        const long long off = live ? (q0 + (int64_t)tok) * p.o_rs + head * p.o_hs : -1;
+        constexpr int LPR = HD / 8;  // lanes per row
+#pragma unroll 4
+        for (int it = 0; it < LPR; ++it) {
+          const int r = it * (32 / LPR) + lane / LPR;
+          const long long ro = __shfl_sync(0xffffffffu, off, r);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * C::STAGE_ROW + (lane % LPR) * 16);
+          if (ro >= 0) *reinterpret_cast<uint4*>(p.o + ro + (lane % LPR) * 8) = v;
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == WARP_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of a split row: O = sum_s w_s O_s / sum_s w_s, w_s = l_s 2^(m_s - max m).
+// One warp per (token, head) row, parts in ascending order.
+template <int HD>
+__global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ Plan plan, const PParams p) {
+  griddep_wait();
+  griddep_trigger();
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (r >= plan.join0[plan.n]) return;
+  int lo = 0, hi = plan.n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (plan.join0[mid] <= r) lo = mid; else hi = mid;
+  }
+  const int H = p.n_kv * p.group;
+  const int rows = plan.q_len[lo] * H, parts = plan.parts[lo];
+  const int rr = r - plan.join0[lo];
+  const int64_t at = (int64_t)plan.part0[lo] + rr;
+  float m = -INFINITY;
+  for (int s = lane; s < parts; s += 32) {
+    const float2 ml = p.part_ml[at + (int64_t)s * rows];
+    if (ml.y != 0.f) m = fmaxf(m, ml.x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  constexpr int V = HD / 32;
+  float acc[V] = {};
+  float den = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) {
+    const float2 ml = p.part_ml[at + (int64_t)s * rows];
+    float v[V];
+    const float* src = p.part_o + (at + (int64_t)s * rows) * HD + lane * V;
+    if constexpr (V == 4) {
+      const float4 f = *reinterpret_cast<const float4*>(src);
+      v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+    } else {
+      const float2 f = *reinterpret_cast<const float2*>(src);
+      v[0] = f.x; v[1] = f.y;
+    }
+    const float w = ml.y == 0.f ? 0.f : ml.y * ex2(ml.x - m);
+    den += w;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+  }
+  const float inv = den == 0.f ? 0.f : 1.0f / den;
+  const int tok = rr / H, head = rr - tok * H;
+  __nv_bfloat16* dst = p.o + (plan.q0[lo] + (int64_t)tok) * p.o_rs + head * p.o_hs + lane * V;
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+}
+
+struct HostPlan {
+  Plan p;
+  int tokens, group, chunk;
+  int64_t q_rows, kv_rows, part_rows;
+  double pairs;  // allowed (query, key) pairs, for the profiler
+};
+
+constexpr int kMinChunk = 4;   // key tiles of a part at least
+constexpr int kSplitGain = 2;  // split only what is this many chunks long
+
+// Items, splits and workspace rows of a call; false on invalid lengths.
+bool make_plan(const zdit_prompt_attention_args& a, HostPlan* h) {
+  if (a.batch <= 0 || a.batch > kMaxSeqs || !a.q_len || a.n_kv_heads <= 0 || a.n_heads <= 0 ||
+      a.n_heads % a.n_kv_heads || a.n_heads / a.n_kv_heads > 64 || (a.head_dim != 64 && a.head_dim != 128) ||
+      a.n_heads > (1 << 16) || a.causal < 0 || a.causal > 1)
+    return false;
+  h->group = a.n_heads / a.n_kv_heads;
+  h->tokens = TILE / h->group;
+  struct Seq { int q0, ql, kv0, kl, tiles; };
+  Seq seq[kMaxSeqs];
+  int n = 0;
+  int64_t q = 0, kv = 0, work = 0;
+  h->kv_rows = 0;
+  h->pairs = 0;
+  int longest = 0;
+  for (int b = 0; b < a.batch; ++b) {
+    const int64_t ql = a.q_len[b], kl = a.kv_len ? a.kv_len[b] : ql, k0 = a.kv_start ? a.kv_start[b] : kv;
+    if (ql < 0 || kl < 0 || k0 < 0 || k0 + kl > (1 << 30) || q + ql > (1 << 30)) return false;
+    if (!a.kv_start) kv += kl;
+    h->kv_rows = std::max(h->kv_rows, k0 + kl);
+    if (ql > 0) {
+      seq[n++] = Seq{(int)q, (int)ql, (int)k0, (int)kl, (int)((kl + TILE - 1) / TILE)};
+      const int64_t tiles = (kl + TILE - 1) / TILE, pairs = (ql + 2 * h->tokens - 1) / (2 * h->tokens);
+      work += tiles * pairs;  // (an upper bound for causal rows)
+      longest = std::max(longest, (int)tiles);
+      const double full = (double)ql * kl;
+      if (!a.causal) h->pairs += full;
+      else if (kl >= ql) h->pairs += full - 0.5 * ql * (ql - 1.0);
+      else h->pairs += 0.5 * kl * (kl + 1.0);
+    }
+    q += ql;
+  }
+  h->q_rows = q;
+  const int64_t ideal = (work * a.n_kv_heads + num_sms() - 1) / num_sms();
+  h->chunk = (int)std::max<int64_t>(ideal, kMinChunk);
+  if (longest <= kSplitGain * h->chunk) h->chunk = std::max(longest, 1);
+  std::sort(seq, seq + n, [](const Seq& x, const Seq& y) { return x.tiles != y.tiles ? x.tiles > y.tiles : x.q0 < y.q0; });
+  int64_t items = 0, parts_rows = 0, join = 0;
+  Plan& p = h->p;
+  p.n = n;
+  for (int i = 0; i < n; ++i) {
+    const Seq& s = seq[i];
+    const int64_t pairs = (s.ql + 2 * h->tokens - 1) / (2 * h->tokens);
+    const int parts = std::max(1, (s.tiles + h->chunk - 1) / h->chunk);
+    p.item0[i] = (int)items;
+    p.q0[i] = s.q0; p.q_len[i] = s.ql; p.kv0[i] = s.kv0; p.kv_len[i] = s.kl; p.parts[i] = parts;
+    p.part0[i] = (int)parts_rows;
+    p.join0[i] = (int)join;
+    items += pairs * parts;
+    if (parts > 1) {
+      join += (int64_t)s.ql * a.n_heads;
+      parts_rows += (int64_t)s.ql * a.n_heads * parts;
+    }
+    if (items * a.n_kv_heads > INT_MAX || parts_rows > INT_MAX || join > INT_MAX) return false;
+  }
+  p.item0[n] = (int)items;
+  p.join0[n] = (int)join;
+  h->part_rows = parts_rows;
+  return true;
+}
+
+size_t plan_bytes(const HostPlan& h, int head_dim) {
+  if (h.part_rows == 0) return 0;
+  const size_t ml = ((size_t)h.part_rows * sizeof(float2) + 255) / 256 * 256;
+  return ml + (size_t)h.part_rows * head_dim * sizeof(float);
+}
+
+template <int HD>
+zdit_status launch_prompt(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const HostPlan& h,
+                          const PParams& p, cudaStream_t s) {
+  using C = Cfg<HD>;
+  // per launch: the opt-in belongs to the current context
+  if (cudaFuncSetAttribute(prompt_attn_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return ZDIT_ERR_CUDA;
+  const int H = p.n_kv * p.group;
+  {
+    ProfScope ps(PROF_ATTENTION, 4.0 * HD * H * h.pairs,
+                 2.0 * HD * (2.0 * H * h.q_rows + 2.0 * p.n_kv * h.kv_rows), s);
+    if (launch_dependent(prompt_attn_kernel<HD>, dim3((unsigned)(h.p.item0[h.p.n] * p.n_kv)), dim3(THREADS), C::SMEM, s,
+                         tq, tk, tv, h.p, p) != cudaSuccess)
+      return ZDIT_ERR_CUDA;
+  }
+  const int join = h.p.join0[h.p.n];
+  if (join > 0) {
+    ProfScope ps(PROF_ATTENTION, 0.0, (4.0 * HD + 8.0) * h.part_rows + 2.0 * HD * join, s);
+    if (launch_dependent(prompt_join_kernel<HD>, dim3((unsigned)((join + 3) / 4)), dim3(128), 0, s, h.p, p) !=
+        cudaSuccess)
+      return ZDIT_ERR_CUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? ZDIT_OK : ZDIT_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace zdit
+
+using namespace zdit;
+
+extern "C" {
+
+ZDIT_API size_t zdit_prompt_attention_workspace_bytes(const zdit_prompt_attention_args* a) {
+  HostPlan h;
+  if (a == nullptr || !make_plan(*a, &h)) return 0;
+  return plan_bytes(h, a->head_dim);
+}
+
+ZDIT_API zdit_status zdit_prompt_attention(const zdit_prompt_attention_args* a, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  if (a == nullptr || !a->q_len) return ZDIT_ERR_INVALID_ARG;
+  if (!(a->scale >= 0.f) || !std::isfinite(a->scale) || a->causal < 0 || a->causal > 1) return ZDIT_ERR_INVALID_ARG;
+  HostPlan h;
+  if (!make_plan(*a, &h)) return ZDIT_ERR_SHAPE;
+  if (h.q_rows > 0 && (!a->q.ptr || !a->o.ptr)) return ZDIT_ERR_INVALID_ARG;
+  if (h.kv_rows > 0 && (!a->k.ptr || !a->v.ptr)) return ZDIT_ERR_INVALID_ARG;
+  const zdit_heads* hs[4] = {&a->q, &a->k, &a->v, &a->o};
+  for (int i = 0; i < 4; ++i) {
+    const int n = (i == 0 || i == 3) ? a->n_heads : a->n_kv_heads;
+    const int64_t rows = (i == 0 || i == 3) ? h.q_rows : h.kv_rows;
+    const int64_t lim = int64_t(1) << 38;  // strides of a tensor map are below 2^40 bytes
+    if ((rows > 1 && (hs[i]->row_stride < a->head_dim || hs[i]->row_stride > lim)) ||
+        (n > 1 && (hs[i]->head_stride < a->head_dim || hs[i]->head_stride > lim)))
+      return ZDIT_ERR_SHAPE;
+    if ((reinterpret_cast<uintptr_t>(hs[i]->ptr) & 15) || (rows > 1 && hs[i]->row_stride % 8) ||
+        (n > 1 && hs[i]->head_stride % 8))
+      return ZDIT_ERR_ALIGNMENT;
+  }
+  if (!heads_disjoint(a->o, h.q_rows, a->n_heads, a->head_dim)) return ZDIT_ERR_SHAPE;
+  const size_t need = plan_bytes(h, a->head_dim);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need) return ZDIT_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255) return ZDIT_ERR_ALIGNMENT;
+  }
+  if (h.q_rows == 0) return ZDIT_OK;
+  if (!device_ok()) return ZDIT_ERR_UNSUPPORTED;
+  PParams p;
+  p.n_kv = a->n_kv_heads; p.group = h.group; p.tokens = h.tokens; p.chunk = h.chunk; p.causal = a->causal;
+  const float scale = a->scale == 0.f ? 1.0f / sqrtf((float)a->head_dim) : a->scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.o = static_cast<__nv_bfloat16*>(a->o.ptr); p.o_rs = a->o.row_stride; p.o_hs = a->o.head_stride;
+  p.part_ml = static_cast<float2*>(workspace);
+  p.part_o = need ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                             ((size_t)h.part_rows * sizeof(float2) + 255) / 256 * 256) : nullptr;
+  p.err = device_error_ptr();
+  CUtensorMap tq, tk, tv;
+  if (h.kv_rows == 0) {
+    // no sequence has a key: no K or V tile is loaded, the maps only have to be valid
+    if (!make_tmap_bf16_heads(&tk, a->q.ptr, 1, 1, a->head_dim, a->head_dim, a->head_dim, 1, TILE)) return ZDIT_ERR_CUDA;
+    tv = tk;
+  } else if (!make_tmap_bf16_heads(&tk, a->k.ptr, h.kv_rows, a->n_kv_heads, a->head_dim, a->k.row_stride,
+                                   a->k.head_stride, 1, TILE) ||
+             !make_tmap_bf16_heads(&tv, a->v.ptr, h.kv_rows, a->n_kv_heads, a->head_dim, a->v.row_stride,
+                                   a->v.head_stride, 1, TILE)) {
+    return ZDIT_ERR_CUDA;
+  }
+  if (!make_tmap_bf16_heads(&tq, a->q.ptr, h.q_rows, a->n_heads, a->head_dim, a->q.row_stride, a->q.head_stride,
+                            h.group, h.tokens))
+    return ZDIT_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return a->head_dim == 64 ? launch_prompt<64>(tq, tk, tv, h, p, s) : launch_prompt<128>(tq, tk, tv, h, p, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,580 @@
+"""Prompt operators on the GPU against 64-bit definitions: scaled rotary tables, query / key
+norm with rotation, attention of packed prompts, projections with their epilogue, and one
+encoder layer made of them whose rows feed the image model.
+
+Tolerances (u = 2^-8, the half step of bf16; 2^-24 that of fp32) are bounds of the
+arithmetic, element by element:
+
+* rope table: the angle is pos * w in fp64 (w off by ~2 ulp, one rounding of the product:
+  3 |pos| 2^-53 < |pos| 2^-51), the reduced angle is rounded to fp32 (2^-25), the fp32 sine
+  and cosine are within 2 ulp (2^-23), the product with the magnitude rounds twice.
+* norm and rotation: sum of squares 13 roundings, root and quotient 2, products 2, rotation
+  3, all below 32 half steps of fp32 on values up to 2 max|x|: 2^-18 max|x| of the head,
+  plus the store.
+* attention: each P is rounded to bf16 (u), and the store rounds once (u).  With A = sum p |v|
+  the error is at most (u (1 + u) + d) A + u |O|, d = what fp32 adds: the logits, products
+  of head_dim terms accumulated at 2^-23 a step, move p by scale (head_dim + 2) 2^-23
+  max_j sum |q k_j| relative, twice (numerator and sum); PV accumulates up to m keys and
+  the sum m / 8 at 2^-23 a step.
+* linear: K / 16 accumulator steps of 2^-23, each on a partial sum below ~4 times the random
+  walk T = sqrt(sum (a w)^2), plus 16 for the steps inside; activations with slope <= 1.13
+  and relative error (exp of y at 2^-22 |y|) 2^-20 (1 + |y|); the store.
+"""
+import numpy as np
+import pytest
+import torch
+
+import stream_diffusion_transformer_s3_b200 as Z
+from _gpu import require_gpu
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -8
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def rnd(seed, *shape, scale=1.0, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def store_u(dtype):
+    return U if dtype == torch.bfloat16 else 2.0 ** -24
+
+
+def check(got, ref, bound, label):
+    assert Z.zdit_device_status() == 0
+    got, ref = got.double(), ref.double()
+    assert torch.isfinite(got).all(), f"{label}: non-finite values"
+    worst = ((got - ref).abs() / bound.clamp_min(1e-300)).max().item() if got.numel() else 0.0
+    print(f"{label}: worst element at {worst:.3f} of its bound")
+    assert worst <= 1.0, f"{label}: {worst:.3f} of the bound"
+
+
+# ------------------------------------------------------------------ rotary tables
+def frequencies(d, theta, sc):
+    i = np.arange(d // 2, dtype=np.longdouble)
+    w = np.longdouble(theta) ** (-2 * i / d)
+    if sc is None or sc.kind == Z.ROPE_SCALE_NONE:
+        return w
+    f = np.longdouble(sc.factor)
+    if sc.kind == Z.ROPE_SCALE_LINEAR:
+        return w / f
+    if sc.kind == Z.ROPE_SCALE_NTK:
+        return (np.longdouble(theta) * f ** (np.longdouble(d) / (d - 2))) ** (-2 * i / d)
+    pi = np.longdouble("3.14159265358979323846264338327950288")
+    turns = np.longdouble(sc.original_len) * w / (2 * pi)
+    g = np.clip((turns - sc.beta_slow) / (np.longdouble(sc.beta_fast) - np.longdouble(sc.beta_slow)), 0, 1)
+    return w * g + w / f * (1 - g)
+
+
+@pytest.mark.parametrize("T,d,theta,sc,first", [
+    (1, 2, 1e4, None, 0),
+    (5, 4, 1e4, Z.RopeScaling(Z.ROPE_SCALE_NTK, 8.0), -3),
+    (77, 128, 1e6, None, 0),
+    (777, 96, 5e5, Z.RopeScaling(Z.ROPE_SCALE_LINEAR, 4.0), 1 << 20),
+    (333, 128, 1e6, Z.RopeScaling(Z.ROPE_SCALE_YARN, 4.0, 32768.0, 32.0, 1.0, 1.1386), 100000),
+    (64, 22, 1e4, Z.RopeScaling(Z.ROPE_SCALE_YARN, 2.0, 2048.0, 32.0, 1.0), 5),   # 11 pairs a row
+    (9, 512, 1e4, Z.RopeScaling(Z.ROPE_SCALE_NTK, 2.0), 12345),
+    (6, 128, 1e4, None, (1 << 31) - 6),                                            # the last positions
+    (3000, 64, 1e4, Z.RopeScaling(), -1500),
+])
+def test_rope_table_scaled(T, d, theta, sc, first):
+    pos = np.arange(first, first + T, dtype=np.int64)
+    cs = torch.full((T + 1, d // 2), 7.0, device="cuda")
+    sn = torch.full((T + 1, d // 2), 7.0, device="cuda")
+    Z.zdit_rope_table_scaled(torch.tensor(pos.astype(np.int32), device="cuda"), d, theta, cs[:T], sn[:T], sc)
+    assert Z.zdit_device_status() == 0
+    ang = pos.astype(np.longdouble)[:, None] * frequencies(d, theta, sc)
+    mag = 1.0 if sc is None else float(sc.magnitude)
+    tol = mag * (2.0 ** -25 + 2.0 ** -23 + 2.0 ** -23 + np.abs(pos)[:, None] * 2.0 ** -51)
+    for got, ref in ((cs, np.cos(ang)), (sn, np.sin(ang))):
+        err = np.abs(got[:T].double().cpu().numpy() - (ref * mag).astype(np.float64))
+        print(f"rope {T}x{d}: {np.max(err / tol):.3f} of the bound")
+        assert (err <= tol).all()
+        assert (got[T] == 7.0).all()
+
+
+def test_rope_table_scaled_agrees_with_the_three_axis_table():
+    pos = torch.arange(50, device="cuda", dtype=torch.int32)
+    a = [torch.empty(50, 64, device="cuda") for _ in range(4)]
+    Z.zdit_rope_table_scaled(pos, 128, 1e4, a[0], a[1])
+    Z.zdit_rope_table(torch.stack([pos, pos, pos], 1).contiguous(), (128, 0, 0), 1e4, a[2], a[3])
+    assert (a[0] - a[2]).abs().max() < 2.0 ** -22 and (a[1] - a[3]).abs().max() < 2.0 ** -22
+
+
+# ------------------------------------------------------------------ query / key norm and rotation
+def norm_rotate(x, w, cos, sin, layout, rot, eps):
+    x = x.double()
+    if w is not None:
+        x = x / (x.square().mean(-1, keepdim=True) + eps).sqrt() * w.double()
+    scale = x.abs().amax(-1, keepdim=True)
+    y = x.clone()
+    if rot:
+        c, s = cos.double()[:, None], sin.double()[:, None]
+        ia = torch.arange(rot // 2, device="cuda")
+        ia, ib = (2 * ia, 2 * ia + 1) if layout == Z.ROPE_INTERLEAVED else (ia, ia + rot // 2)
+        y[..., ia] = x[..., ia] * c - x[..., ib] * s
+        y[..., ib] = x[..., ia] * s + x[..., ib] * c
+    return y, scale
+
+
+def tables(T, rot, seed=3):
+    ang = torch.rand(T, rot // 2, generator=torch.Generator().manual_seed(seed)).double() * 100
+    return ang.cos().float().cuda(), ang.sin().float().cuda()
+
+
+@pytest.mark.parametrize("layout", [Z.ROPE_HALF, Z.ROPE_INTERLEAVED])
+@pytest.mark.parametrize("T,nq,nk,hd,rot,src,dst,norm", [
+    (1, 1, 0, 8, 8, "f", "b", True),
+    (1, 32, 8, 128, 128, "b", "b", True),
+    (133, 32, 8, 128, 128, "f", "b", True),
+    (257, 5, 5, 128, 32, "b", "b", True),       # a quarter of the head
+    (64, 7, 1, 64, 64, "b", "f", True),
+    (33, 3, 2, 80, 40, "b", "b", True),         # head of 10 lanes, halves of 20 elements
+    (50, 6, 2, 96, 96, "f", "f", True),
+    (50, 6, 2, 96, 6, "b", "b", True),          # 3 pairs
+    (19, 2, 1, 256, 128, "b", "b", True),
+    (19, 2, 1, 256, 256, "f", "b", False),
+    (40, 4, 4, 128, 0, "b", "b", True),         # norm only
+    (40, 4, 4, 64, 64, "b", "b", False),        # rotation only
+])
+def test_qk_norm_rope(T, nq, nk, hd, rot, src, dst, norm, layout):
+    ty = {"f": torch.float32, "b": torch.bfloat16}
+    row = (nq + 2 * nk) * hd + 16  # q | k | v | something else
+    qkv = rnd(T * hd + rot, T, row, scale=3.0, dtype=ty[src])
+    q, k = qkv[:, :nq * hd].view(T, nq, hd), qkv[:, nq * hd:(nq + nk) * hd].view(T, nk, hd)
+    wq = 1 + 0.3 * rnd(1, hd, dtype=torch.float32) if norm else None
+    wk = 1 + 0.3 * rnd(2, hd, dtype=torch.float32) if norm else None
+    cos, sin = tables(T, rot) if rot else (None, None)
+    qo = torch.full((T + 1, nq, hd), 99.0, device="cuda", dtype=ty[dst])
+    ko = torch.full((nk, T + 1, hd), 99.0, device="cuda", dtype=ty[dst])  # head-major, as a cache may be
+    Z.zdit_qk_norm_rope(q, k if nk else None, qo[:T], ko.transpose(0, 1)[:T] if nk else None, wq, wk, cos, sin, rot,
+                        layout, eps=1e-6)
+    for got, x, w, n in ((qo[:T], q, wq, nq), (ko.transpose(0, 1)[:T], k, wk, nk)):
+        if n == 0:
+            continue
+        ref, scale = norm_rotate(x, w, cos, sin, layout, rot, 1e-6)
+        check(got, ref, store_u(ty[dst]) * ref.abs() + 2.0 ** -18 * scale, f"qk {T}x{n}x{hd}/{rot}")
+    assert (qo[T] == 99).all() and (ko[:, T] == 99).all()
+
+
+def test_qk_norm_rope_in_place_touches_only_its_heads():
+    T, nq, nk, hd = 61, 8, 2, 128
+    qkv = rnd(5, T, (nq + 2 * nk) * hd)
+    before = qkv.clone()
+    q, k = qkv[:, :nq * hd].view(T, nq, hd), qkv[:, nq * hd:(nq + nk) * hd].view(T, nk, hd)
+    w = 1 + 0.3 * rnd(1, hd, dtype=torch.float32)
+    cos, sin = tables(T, hd)
+    apart = [torch.empty(T, n, hd, device="cuda", dtype=torch.bfloat16) for n in (nq, nk)]
+    Z.zdit_qk_norm_rope(q, k, *apart, w, w, cos, sin, hd)
+    Z.zdit_qk_norm_rope(q, k, q, k, w, w, cos, sin, hd)
+    assert torch.equal(q, apart[0]) and torch.equal(k, apart[1])
+    assert torch.equal(qkv[:, (nq + nk) * hd:], before[:, (nq + nk) * hd:])
+
+
+def test_qk_norm_rope_zero_and_large_rows():
+    # a head of zeros stays zero (eps), one near the largest bf16 does not overflow its sum
+    T, hd = 4, 128
+    q = torch.zeros(T, 1, hd, device="cuda", dtype=torch.bfloat16)
+    q[1] = 1e18
+    q[2] = 3e-20
+    q[3, 0, ::2] = -5.0
+    cos, sin = tables(T, hd)
+    out = torch.empty_like(q)
+    Z.zdit_qk_norm_rope(q, None, out, None, torch.ones(hd, device="cuda"), None, cos, sin, hd)
+    ref, scale = norm_rotate(q, torch.ones(hd, device="cuda"), cos, sin, Z.ROPE_HALF, hd, 1e-6)
+    check(out, ref, U * ref.abs() + 2.0 ** -18 * scale, "qk extremes")
+    assert (out[0] == 0).all()
+
+
+# ------------------------------------------------------------------ attention
+def attention_ref(q, k, v, q_len, kv_len, kv_start, causal, scale):
+    """(O, bound) of the definition in 64 bits, per sequence and head."""
+    H, Hkv, hd = q.shape[1], k.shape[1], q.shape[2]
+    O = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    B = torch.zeros_like(O)
+    t0 = 0
+    for n, m, s0 in zip(q_len, kv_len, kv_start):
+        if n and m:
+            ks, vs = k[s0:s0 + m].double(), v[s0:s0 + m].double()
+            for h in range(H):
+                qh, kh, vh = q[t0:t0 + n, h].double(), ks[:, h * Hkv // H], vs[:, h * Hkv // H]
+                x = qh @ kh.T * scale
+                ok = torch.ones(n, m, dtype=torch.bool, device="cuda")
+                if causal:
+                    ok = ok.tril(m - n)
+                x = x.masked_fill(~ok, -torch.inf)
+                p = torch.exp(x - x.amax(-1, keepdim=True).clamp_min(-1e300)).masked_fill(~ok, 0.0)
+                den = p.sum(-1, keepdim=True)
+                p = torch.where(den > 0, p / den.clamp_min(1e-300), torch.zeros_like(p))
+                O[t0:t0 + n, h] = p @ vh
+                A = p @ vh.abs()
+                dl = scale * (hd + 2) * 2.0 ** -23 * (qh.abs() @ kh.abs().T).amax(-1, keepdim=True)
+                d = 2 * dl + (2 * m + 64) * 2.0 ** -23
+                B[t0:t0 + n, h] = (U * (1 + U) + d) * A + U * O[t0:t0 + n, h].abs()
+        t0 += n
+    return O, B
+
+
+def run_attention(q_len, kv_len=None, kv_start=None, H=8, Hkv=2, hd=128, causal=True, seed=0, scale=0.0, gap=0,
+                  qscale=1.0, head_major=False, label=""):
+    """One call on inputs with NaN in every row of k and v that no sequence owns and a
+    sentinel in the rows of o behind the last sequence; returns o."""
+    lens = q_len if kv_len is None else kv_len
+    starts = kv_start if kv_start is not None else [sum(lens[:b]) for b in range(len(lens))]
+    T, R = sum(q_len), max([s + m for s, m in zip(starts, lens)] + [0]) + gap
+    q = rnd(seed + 1, T + 2, H, hd, scale=qscale)
+    k, v = rnd(seed + 2, R, Hkv, hd), rnd(seed + 3, R, Hkv, hd)
+    owned = torch.zeros(R, dtype=torch.bool)
+    for s, m in zip(starts, lens):
+        owned[s:s + m] = True
+    k[~owned.cuda()] = torch.nan
+    v[~owned.cuda()] = torch.nan
+    if head_major:
+        k, v = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (k, v))
+        q = q.transpose(0, 1).contiguous().transpose(0, 1)
+    q[T:] = torch.nan
+    o = torch.full((T + 3, H, hd), 17.0, device="cuda", dtype=torch.bfloat16)
+    if head_major:
+        o = o.transpose(0, 1).contiguous().transpose(0, 1)
+    batch = Z.PromptBatch(q_len, kv_len, kv_start)
+    need = Z.prompt_attention_workspace_bytes(batch, H, Hkv, hd, causal)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda") if need else None  # NaN patterns
+    Z.zdit_prompt_attention(q, k, v, o, batch, ws, causal=causal, scale=scale)
+    sc = scale if scale else hd ** -0.5
+    ref, bound = attention_ref(q[:T], k, v, q_len, lens, starts, causal, sc)
+    check(o[:T], ref, bound, label or f"attention q {q_len} kv {lens} {H}/{Hkv}x{hd} split {need > 0}")
+    assert (o[T:] == 17.0).all()
+    return o, (q, k, v, batch, ws)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("q_len,H,Hkv", [
+    ((1,), 1, 1),
+    ((1, 2, 3), 4, 1),
+    ((127, 128, 129), 2, 2),               # a tile less one, a tile, a tile and one
+    ((255, 1, 257), 3, 3),                 # pairs of tiles
+    ((31, 32, 33, 64, 65), 8, 2),          # groups of 4: tiles of 32 tokens
+    ((40, 43), 6, 2),                      # groups of 3: 42 tokens and 2 unused rows
+    ((10, 300), 14, 2),                    # groups of 7
+    ((50,), 64, 1),                        # 64 heads on one key head: 2 tokens a tile
+    ((0, 5, 0, 9), 4, 4),                  # empty sequences
+    ((1000, 7), 4, 2),
+])
+def test_prompt_attention_whole_prompts(q_len, H, Hkv, hd):
+    run_attention(q_len, H=H, Hkv=Hkv, hd=hd, gap=3, seed=sum(q_len))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("q_len,kv_len,kv_start", [
+    ((1, 1, 1), (1, 128, 129), None),                       # single tokens
+    ((1, 1), (5000, 4097), (0, 6000)),                      # split keys, slots with a gap
+    ((3, 17), (900, 2000), (5, 905)),
+    ((37, 37, 37), (1500, 1500, 1500), (0, 0, 0)),          # the same prefix three times
+    ((200, 1), (1000, 3000), (3000, 0)),                    # slots in another order
+    ((5, 4, 3), (0, 2, 3), (0, 0, 2)),                      # no keys; fewer keys than rows
+    ((300,), (130,), (0,)),                                 # first rows see nothing
+    ((2,), (9001,), (77,)),
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_attention_prefixes_and_single_tokens(q_len, kv_len, kv_start, hd, causal):
+    run_attention(q_len, kv_len, kv_start, H=8, Hkv=2, hd=hd, causal=causal, gap=200, seed=sum(kv_len))
+
+
+def test_prompt_attention_rows_without_keys_are_zero():
+    o, _ = run_attention((300,), (130,), (0,), H=4, Hkv=2)
+    assert (o[:170] == 0).all() and (o[170:300] != 0).any()
+    o, _ = run_attention((5,), (0,), (0,), H=4, Hkv=2)
+    assert (o[:5] == 0).all()
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_prompt_attention_head_major_buffers(hd):
+    run_attention((70, 133), H=6, Hkv=3, hd=hd, head_major=True)
+    run_attention((1, 1), (700, 3000), (0, 700), H=6, Hkv=3, hd=hd, head_major=True)
+
+
+def test_prompt_attention_scale_and_peaked_rows():
+    run_attention((200,), H=4, Hkv=1, scale=0.5)
+    run_attention((64, 300), H=4, Hkv=2, qscale=8.0)       # a row's weight on few keys
+    run_attention((1,), (6000,), (0,), H=8, Hkv=1, qscale=8.0)
+
+
+def test_prompt_attention_reference_maximum_moves():
+    # logits that grow along the keys by far more than the rescale threshold, and shrink
+    for sign in (1.0, -1.0):
+        n, H, hd = 700, 2, 128
+        q = torch.full((n, H, hd), 0.5, device="cuda", dtype=torch.bfloat16)
+        ramp = sign * torch.linspace(0, 6, n, device="cuda")[:, None, None]
+        k = (rnd(3, n, H, hd, dtype=torch.float32) * 0.1 + ramp).bfloat16()
+        v = rnd(4, n, H, hd)
+        for rows in (n, 1):
+            o = torch.empty(rows, H, hd, device="cuda", dtype=torch.bfloat16)
+            b = Z.PromptBatch([rows], [n])
+            Z.zdit_prompt_attention(q[:rows], k, v, o, b, None if rows > 1 else torch.empty(
+                Z.prompt_attention_workspace_bytes(b, H, H, hd), dtype=torch.uint8, device="cuda"))
+            ref, bound = attention_ref(q[:rows], k, v, [rows], [n], [0], True, hd ** -0.5)
+            check(o, ref, bound, f"moving maximum {sign} {rows}")
+
+
+def test_prompt_attention_long_prompt():
+    run_attention((4500, 700), H=4, Hkv=1, seed=9)
+
+
+def test_prompt_attention_equals_joint_attention_without_mask():
+    lengths, H = (130, 333), 3
+    T = sum(lengths)
+    q, k, v = (rnd(i, T, H, 128) for i in (1, 2, 3))
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    Z.zdit_prompt_attention(q, k, v, a, Z.PromptBatch(lengths), causal=False)
+    Z.zdit_joint_attention(q.view(T, -1), k.view(T, -1), v.view(T, -1), b.view(T, -1), Z.DeviceVarlen([0, 130, T]), H)
+    ref, bound = attention_ref(q, k, v, lengths, lengths, (0, 130), False, 128 ** -0.5)
+    check(a, ref, bound, "unmasked")
+    check(b, ref, bound, "joint attention")
+
+
+def test_prompt_attention_is_deterministic_and_replays():
+    # a split call: the same bits every time, eager, on another stream and from a graph
+    o, (q, k, v, batch, ws) = run_attention((1, 2, 1), (5000, 777, 3000), (0, 5000, 6000), H=8, Hkv=2)
+    first = o[:4].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        o2 = torch.zeros_like(o)
+        Z.zdit_prompt_attention(q, k, v, o2, batch, ws)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(o2[:4], first)
+    o3 = torch.zeros_like(o)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        Z.zdit_prompt_attention(q, k, v, o3, batch, ws)
+    for _ in range(3):
+        o3.zero_()
+        g.replay()
+        assert torch.equal(o3[:4], first)
+    # replayed on new data in the same buffers
+    q.mul_(0.5)
+    g.replay()
+    ref, bound = attention_ref(q[:4], k, v, [1, 2, 1], [5000, 777, 3000], [0, 5000, 6000], True, 128 ** -0.5)
+    check(o3[:4], ref, bound, "replay on new data")
+
+
+def test_prompt_attention_far_row_offsets():
+    # key rows whose offsets pass 2^31 elements: 33 M rows of one head, the last ones used
+    rows, hd = (1 << 25) + 1000, 64
+    k = torch.empty(rows, 1, hd, device="cuda", dtype=torch.bfloat16)
+    v = torch.empty(rows, 1, hd, device="cuda", dtype=torch.bfloat16)
+    start = rows - 900
+    k[start:], v[start:] = rnd(1, 900, 1, hd), rnd(2, 900, 1, hd)
+    q = rnd(3, 40, 2, hd)
+    o = torch.empty_like(q)
+    b = Z.PromptBatch([40], [900], [start])
+    ws = torch.empty(Z.prompt_attention_workspace_bytes(b, 2, 1, hd), dtype=torch.uint8, device="cuda")
+    Z.zdit_prompt_attention(q, k, v, o, b, ws)
+    ref, bound = attention_ref(q, k[start:], v[start:], [40], [900], [0], True, hd ** -0.5)
+    check(o, ref, bound, "far rows")
+
+
+# ------------------------------------------------------------------ linear
+def linear_ref(a, w, bias, act, residual, exact_product=False):
+    A, W = a.double(), w.double()
+    y = A @ W.T
+    T = (A.square() @ W.square().T).sqrt()
+    K = a.shape[1]
+    e = (0.0 if exact_product else 4 * (K / 16 + 16) * 2.0 ** -23) * T
+    if bias is not None:
+        y = y + bias.double()
+        e = e + 2.0 ** -23 * y.abs()
+    f = y
+    if act == Z.ACT_SILU:
+        f = y * torch.sigmoid(y)
+    elif act == Z.ACT_GELU:
+        f = 0.5 * y * torch.special.erfc(-y / 2 ** 0.5)
+    elif act == Z.ACT_GELU_TANH:
+        f = y * torch.sigmoid(2 * (2 / np.pi) ** 0.5 * (y + 0.044715 * y ** 3))
+    if act != Z.ACT_NONE:
+        # relative error of the exponential: its argument (y, or up to ~1.6 y (1 + y^2 / 22)
+        # for the tanh form) in fp32, and 2^-22 of the function itself
+        arg = y.abs() * (1 + (0.1 * y.square() if act == Z.ACT_GELU_TANH else y.abs() if act == Z.ACT_GELU else 0))
+        e = 1.13 * e + 2.0 ** -20 * (1 + arg) * f.abs()
+    if residual is not None:
+        f = f + residual.double()
+        e = e + 2.0 ** -23 * (f.abs() + residual.double().abs())
+    return f, e
+
+
+SHAPES = [
+    (1, 1, 1), (1, 1, 8), (3, 5, 7), (1, 2560, 4096), (5, 2560, 4096), (16, 129, 64), (17, 256, 65), (33, 300, 1000),
+    (64, 1024, 2560), (65, 2560, 320), (133, 9728, 256), (128, 128, 128), (200, 777, 2560), (257, 255, 250),
+    (600, 1111, 2563), (1000, 512, 64), (2049, 640, 3840),
+]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("act,bias,res,out", [
+    (Z.ACT_NONE, False, None, "f"),
+    (Z.ACT_SILU, True, None, "b"),
+    (Z.ACT_GELU, True, "f", "b"),
+    (Z.ACT_GELU_TANH, False, "b", "f"),
+])
+def test_linear(M, N, K, act, bias, res, out):
+    ty = {"f": torch.float32, "b": torch.bfloat16}
+    Kp = (K + 7) // 8 * 8 + 8
+    a, w = rnd(1, M, Kp), rnd(2, N, Kp, scale=K ** -0.5)
+    a[:, K:], w[:, K:] = torch.nan, torch.nan  # columns past K are never used
+    a, w = a[:, :K], w[:, :K]
+    b = rnd(3, N, dtype=torch.float32) if bias else None
+    r = rnd(4, M, N + 3, scale=2.0, dtype=ty[res])[:, :N] if res else None
+    o = torch.full((M + 1, N + 5), 9.0, device="cuda", dtype=ty[out])
+    Z.zdit_linear(a, w, o[:M, :N], bias=b, act=act, residual=r)
+    ref, e = linear_ref(a, w, b, act, r)
+    check(o[:M, :N], ref, e + store_u(ty[out]) * ref.abs(), f"linear {M}x{N}x{K} act {act}")
+    assert (o[M] == 9).all() and (o[:, N:] == 9).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 2560, 512), (133, 520, 2560), (700, 768, 1024)])
+@pytest.mark.parametrize("ty", [torch.bfloat16, torch.float32])
+def test_linear_residual_in_place(M, N, K, ty):
+    a, w, x = rnd(1, M, K), rnd(2, N, K, scale=K ** -0.5), rnd(3, M, N, dtype=ty)
+    ref, e = linear_ref(a, w, None, Z.ACT_NONE, x)
+    Z.zdit_linear(a, w, x, residual=x)
+    check(x, ref, e + store_u(ty) * ref.abs(), "residual in place")
+
+
+@pytest.mark.parametrize("act", [Z.ACT_SILU, Z.ACT_GELU, Z.ACT_GELU_TANH])
+def test_linear_activation_tails(act):
+    # values from -60 to 60 through an identity product
+    n = 64
+    y = torch.linspace(-60, 60, n, device="cuda").bfloat16()
+    a = y[:, None] * torch.eye(n, device="cuda", dtype=torch.bfloat16)
+    o = torch.empty(n, n, device="cuda")
+    Z.zdit_linear(a, torch.eye(n, device="cuda", dtype=torch.bfloat16), o, act=act)
+    ref, e = linear_ref(a, torch.eye(n, device="cuda", dtype=torch.bfloat16), None, act, None, exact_product=True)
+    # products are exact here: only the activation's own error counts, and fp32's smallest values
+    check(o, ref, e + 2.0 ** -24 * ref.abs() + 2.0 ** -126, "tails")
+
+
+def test_linear_is_deterministic_and_replays():
+    a, w = rnd(1, 5, 4096), rnd(2, 2560, 4096, scale=1 / 64)
+    x = rnd(3, 5, 2560, dtype=torch.float32)
+    o = [torch.empty_like(x) for _ in range(2)]
+    Z.zdit_linear(a, w, o[0], residual=x)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        Z.zdit_linear(a, w, o[1], residual=x)
+    for _ in range(3):
+        o[1].zero_()
+        g.replay()
+        assert torch.equal(o[0], o[1])
+
+
+# ------------------------------------------------------------------ together
+class Layer:
+    """Attention half of a causal prompt layer, in 64 bits with the library's roundings left
+    out, and through the library."""
+
+    def __init__(self, D, H, Hkv, hd):
+        self.D, self.H, self.Hkv, self.hd = D, H, Hkv, hd
+        self.w_qkv = rnd(11, (H + 2 * Hkv) * hd, D, scale=D ** -0.5)
+        self.w_o = rnd(12, D, H * hd, scale=(H * hd) ** -0.5)
+        self.nq, self.nk = (1 + 0.2 * rnd(s, hd, dtype=torch.float32) for s in (13, 14))
+
+    def exact(self, x, pos, q_len):
+        H, Hkv, hd = self.H, self.Hkv, self.hd
+        T = x.shape[0]
+        qkv = x.double() @ self.w_qkv.double().T
+        q, k, v = (qkv[:, a:b].reshape(T, -1, hd) for a, b in ((0, H * hd), (H * hd, (H + Hkv) * hd),
+                                                               ((H + Hkv) * hd, (H + 2 * Hkv) * hd)))
+        ang = pos.double()[:, None] * 1e6 ** (-torch.arange(hd // 2, device="cuda", dtype=torch.float64) * 2 / hd)
+        q, _ = norm_rotate(q, self.nq, ang.cos(), ang.sin(), Z.ROPE_HALF, hd, 1e-6)
+        k, _ = norm_rotate(k, self.nk, ang.cos(), ang.sin(), Z.ROPE_HALF, hd, 1e-6)
+        starts = [sum(q_len[:b]) for b in range(len(q_len))]
+        o, _ = attention_ref(q, k, v, q_len, q_len, starts, True, hd ** -0.5)
+        return x.double() + o.reshape(T, -1) @ self.w_o.double().T
+
+    def run(self, x, x16, pos, q_len, out, buf):
+        H, Hkv, hd = self.H, self.Hkv, self.hd
+        T = x.shape[0]
+        qkv, cos, sin, o = buf
+        Z.zdit_rope_table_scaled(pos, hd, 1e6, cos, sin)
+        Z.zdit_linear(x16, self.w_qkv, qkv)
+        q, k, v = (qkv[:, a:b].view(T, -1, hd) for a, b in ((0, H * hd), (H * hd, (H + Hkv) * hd),
+                                                            ((H + Hkv) * hd, (H + 2 * Hkv) * hd)))
+        Z.zdit_qk_norm_rope(q, k, q, k, self.nq, self.nk, cos, sin, hd, Z.ROPE_HALF)
+        Z.zdit_prompt_attention(q, k, v, o, Z.PromptBatch(q_len))
+        Z.zdit_linear(o.view(T, -1), self.w_o, out, residual=x)
+
+
+@pytest.mark.parametrize("q_len", [(45, 1), (300, 7, 41)])
+def test_prompt_layer_feeds_the_image_model(q_len):
+    L = Layer(128, 4, 2, 64)
+    T = sum(q_len)
+    x16 = rnd(20, T, L.D)
+    x = x16.float()
+    pos = torch.cat([torch.arange(n) for n in q_len]).to(device="cuda", dtype=torch.int32)
+    out = torch.empty_like(x)
+    buf = (torch.empty(T, 8 * 64, device="cuda", dtype=torch.bfloat16), torch.empty(T, 32, device="cuda"),
+           torch.empty(T, 32, device="cuda"), torch.empty(T, 4, 64, device="cuda", dtype=torch.bfloat16))
+    L.run(x, x16, pos, q_len, out, buf)
+    assert Z.zdit_device_status() == 0
+    ref = L.exact(x, pos, q_len)
+    # the update carries 4 bf16 roundings (projected row, rotated head, P, attention row): u sqrt(4 / 3)
+    # of its scale on average; 4 u bounds the ratio of the norms
+    err = (out.double() - ref).norm() / (ref - x.double()).norm()
+    print(f"layer update rel {err:.2e}")
+    assert err < 4 * U
+    # the same run from a graph gives the same bits
+    again = torch.zeros_like(out)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        L.run(x, x16, pos, q_len, again, buf)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        L.run(x, x16, pos, q_len, again, buf)
+    again.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again, out)
+    if len(q_len) == 2:
+        # the rows are caption features of the image model
+        from stream_diffusion_transformer_s3_b200 import synth
+        d = synth.BlockDims(dim=256, n_heads=2, head_dim=128, ffn_hidden=384)
+        W = synth.stack_weights(0, d, n_noise=1, n_context=1, n_main=1, cap_dim=128)
+        case = synth.stack_case(0, 8, 8, [64, 32], list(q_len), [0.5, 0.5], cap_dim=128)
+        import oracle as O
+        case["caps"] = out.cpu().numpy()
+        dims = Z.Dims(dim=256, n_heads=2, ffn_hidden=384)
+        stack = Z.DeviceStack(W, dims, 1, 1, 1, patch_dim=64, cap_dim=128)
+        patches = torch.as_tensor(np.ascontiguousarray(case["patches"]), dtype=torch.float32).cuda()
+        call = Z.StackCall(case["grid"], case["n_caps"], case["n_valids"], case["t"], patches, out)
+        ws = torch.empty(Z.stack_workspace_bytes(stack, call), dtype=torch.uint8, device="cuda")
+        vel = torch.empty(2, 64, 64, device="cuda")
+        Z.zdit_stack_forward(stack, call, vel, ws)
+        assert Z.zdit_device_status() == 0
+        want = O.stack_forward(case, W, d)
+        got = vel.double().cpu().numpy()
+        assert np.linalg.norm(got - want) / np.linalg.norm(want) <= 2e-2
+
+
+def test_prompt_rows_of_a_later_call_match_the_whole_prompt():
+    # the prompt in one call, or as a kept prefix, a middle and single tokens over the cache
+    H, Hkv, hd, n = 8, 2, 128, 400
+    q, k, v = rnd(1, n, H, hd), rnd(2, n, Hkv, hd), rnd(3, n, Hkv, hd)
+    whole = torch.empty_like(q)
+    Z.zdit_prompt_attention(q, k, v, whole, Z.PromptBatch([n]))
+    parts = torch.empty_like(q)
+    at = 0
+    for m in (250, 147, 1, 1, 1):
+        b = Z.PromptBatch([m], [at + m])
+        need = Z.prompt_attention_workspace_bytes(b, H, Hkv, hd)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        Z.zdit_prompt_attention(q[at:at + m], k, v, parts[at:at + m], b, ws)
+        at += m
+    ref, bound = attention_ref(q, k, v, [n], [n], [0], True, hd ** -0.5)
+    check(whole, ref, bound, "whole")
+    check(parts, ref, bound, "in parts")
