@@ -184,10 +184,27 @@ def _ptr(t):
     return None if t is None else C.c_void_p(t.data_ptr())
 
 
+_torch = None
+
+
+def _th():
+    """torch, imported on the first call that needs it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _stream(stream=None):
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return C.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return C.c_void_p(stream.cuda_stream)
+    T = _th()
+    raw = getattr(T._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None and T.cuda.is_initialized():
+        # the current stream's handle without building a Stream object (0.1 instead of 3 us)
+        return C.c_void_p(raw(T.cuda.current_device()))
+    return C.c_void_p(T.cuda.current_stream().cuda_stream)
 
 
 # ---------------------------------------------------------------- python-side config
@@ -356,85 +373,82 @@ def zdit_device_status(stream=None):
 # These take torch tensors of any strides the C calls allow.  What the C structs cannot
 # carry (element types, shapes, the device) is checked here.
 def _dtype_code(t, where):
-    import torch
-    if t.dtype == torch.bfloat16:
+    T = _th()
+    dt = t.dtype
+    if dt is T.bfloat16:
         return 0
-    if t.dtype == torch.float32:
+    if dt is T.float32:
         return 1
-    raise ValueError(f"{where}: {t.dtype} is neither bfloat16 nor float32")
+    raise ValueError(f"{where}: {dt} is neither bfloat16 nor float32")
 
 
 def _on_device(where, *tensors):
-    import torch
-    dev = torch.cuda.current_device()
+    dev = _th().cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{where}: tensor on {t.device}, current device is cuda:{dev}")
 
 
-def _f32_vector(where, name, t, n):
-    import torch
-    if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (n,) or not t.is_contiguous()):
-        raise ValueError(f"{where}: {name} must be a contiguous float32 [{n}]")
+def _f32(where, name, t, *shape):
+    """Address of a contiguous fp32 tensor of that shape, None of None."""
+    if t is None:
+        return None
+    if t.dtype is not _th().float32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be a contiguous float32 {list(shape)}")
+    return t.data_ptr()
 
 
-def _heads(where, name, t, shape=None):
+def _heads(where, name, t, shape):
     """Heads struct of a [rows, heads, head_dim] tensor whose last axis is contiguous."""
-    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {shape or '[rows, heads, head_dim]'}")
-    st = t.stride()
-    if st[2] != 1:
+    if len(shape) != 3 or t.shape != shape:
+        raise ValueError(f"{where}: {name} has shape {list(t.shape)}, expected [rows, heads, head_dim] = {list(shape)}")
+    rs, hs, es = t.stride()
+    if es != 1 and shape[2] > 1:
         raise ValueError(f"{where}: {name}'s last axis must be contiguous")
-    return Heads(t.data_ptr(), st[0], st[1])
+    return Heads(t.data_ptr(), rs, hs)
 
 
 def zdit_rope_table_scaled(pos, rotary_dim, theta, cos_out, sin_out, scaling: RopeScaling = None, stream=None):
     """cos / sin [T, rotary_dim / 2] (fp32) of one int32 position per token."""
-    import torch
     w = "zdit_rope_table_scaled"
-    T = pos.shape[0]
-    if pos.dtype != torch.int32 or pos.dim() != 1 or not pos.is_contiguous():
+    if pos.dtype is not _th().int32 or pos.dim() != 1 or not pos.is_contiguous():
         raise ValueError(f"{w}: pos must be a contiguous int32 vector")
-    for t in (cos_out, sin_out):
-        if t.dtype != torch.float32 or tuple(t.shape) != (T, rotary_dim // 2) or not t.is_contiguous():
-            raise ValueError(f"{w}: cos_out and sin_out must be contiguous float32 [{T}, {rotary_dim // 2}]")
+    T = pos.shape[0]
+    pc, ps = _f32(w, "cos_out", cos_out, T, rotary_dim // 2), _f32(w, "sin_out", sin_out, T, rotary_dim // 2)
     _on_device(w, pos, cos_out, sin_out)
     if T == 0:
         return
     _check(lib().zdit_rope_table_scaled(pos.data_ptr(), T, rotary_dim, theta,
-                                        C.byref(scaling) if scaling is not None else None, cos_out.data_ptr(),
-                                        sin_out.data_ptr(), _stream(stream)), w)
+                                        C.byref(scaling) if scaling is not None else None, pc, ps,
+                                        _stream(stream)), w)
 
 
 def zdit_qk_norm_rope(q, k, q_out, k_out, w_q, w_k, cos, sin, rotary_dim, layout=ROPE_HALF, eps=1e-6, stream=None):
     """Per-head RMSNorm (w_q / w_k fp32 [head_dim], None: no norm) and rotation of q [T, n_q,
     head_dim] and k [T, n_k, head_dim] (k and k_out may be None) into q_out, k_out (which may
     be q and k themselves)."""
-    import torch
     w = "zdit_qk_norm_rope"
     T, n_q, hd = q.shape
-    a = QkNormRopeArgs(T=T, n_q=n_q, n_k=0, head_dim=hd, in_dtype=_dtype_code(q, w), out_dtype=_dtype_code(q_out, w),
-                       eps=eps, rotary_dim=rotary_dim, layout=layout)
-    a.q, a.q_out = _heads(w, "q", q), _heads(w, "q_out", q_out, q.shape)
+    hq, hqo = _heads(w, "q", q, (T, n_q, hd)), _heads(w, "q_out", q_out, (T, n_q, hd))
     if (k is None) != (k_out is None):
         raise ValueError(f"{w}: k and k_out go together")
+    n_k, hk, hko = 0, Heads(), Heads()
     if k is not None:
-        if k.dtype != q.dtype or k_out.dtype != q_out.dtype or k.shape[0] != T or k.shape[2] != hd:
-            raise ValueError(f"{w}: k must match q in type, rows and head_dim, k_out must match q_out in type")
-        a.n_k = k.shape[1]
-        a.k, a.k_out = _heads(w, "k", k), _heads(w, "k_out", k_out, k.shape)
-    _f32_vector(w, "w_q", w_q, hd)
-    _f32_vector(w, "w_k", w_k, hd)
+        n_k = k.shape[1]
+        if k.dtype is not q.dtype or k_out.dtype is not q_out.dtype:
+            raise ValueError(f"{w}: k must have q's type and k_out q_out's")
+        hk, hko = _heads(w, "k", k, (T, n_k, hd)), _heads(w, "k_out", k_out, (T, n_k, hd))
+    pq, pk = _f32(w, "w_q", w_q, hd), _f32(w, "w_k", w_k, hd)
+    pc, ps = None, None
     if rotary_dim:
-        for t in (cos, sin):
-            if t is None or t.dtype != torch.float32 or tuple(t.shape) != (T, rotary_dim // 2) or not t.is_contiguous():
-                raise ValueError(f"{w}: cos and sin must be contiguous float32 [{T}, {rotary_dim // 2}]")
-        a.cos, a.sin = cos.data_ptr(), sin.data_ptr()
+        if cos is None or sin is None:
+            raise ValueError(f"{w}: a rotation needs cos and sin")
+        pc, ps = _f32(w, "cos", cos, T, rotary_dim // 2), _f32(w, "sin", sin, T, rotary_dim // 2)
+    a = QkNormRopeArgs(T, n_q, n_k, hd, _dtype_code(q, w), _dtype_code(q_out, w), hq, hk, hqo, hko, pq, pk, eps, pc, ps,
+                       rotary_dim, layout)
     _on_device(w, q, k, q_out, k_out, w_q, w_k, cos, sin)
     if T == 0:
         return
-    a.w_q = w_q.data_ptr() if w_q is not None else None
-    a.w_k = w_k.data_ptr() if w_k is not None else None
     _check(lib().zdit_qk_norm_rope(C.byref(a), _stream(stream)), w)
 
 
@@ -455,10 +469,9 @@ class PromptBatch:
         ends = [s + m for s, m in zip(self.kv_start, lens)] if kv_start is not None else [sum(lens)]
         self.kv_rows = max(ends) if ends else 0
 
-    def args(self, n_heads, n_kv_heads, head_dim, causal, scale):
-        return PromptAttentionArgs(batch=self.batch, q_len=self.q_len, kv_len=self.kv_len, kv_start=self.kv_start,
-                                   n_heads=n_heads, n_kv_heads=n_kv_heads, head_dim=head_dim,
-                                   causal=1 if causal else 0, scale=scale)
+    def args(self, n_heads, n_kv_heads, head_dim, causal, scale, *heads):
+        return PromptAttentionArgs(self.batch, self.q_len, self.kv_len, self.kv_start, n_heads, n_kv_heads, head_dim,
+                                   1 if causal else 0, scale, *heads)
 
 
 def prompt_attention_workspace_bytes(batch: PromptBatch, n_heads, n_kv_heads, head_dim, causal=True) -> int:
@@ -470,46 +483,44 @@ def zdit_prompt_attention(q, k, v, o, batch: PromptBatch, workspace=None, causal
     """Attention of packed prompts: q, o [rows, n_heads, head_dim], k, v [rows, n_kv_heads,
     head_dim], bf16, any row and head strides.  workspace: a uint8 tensor of
     prompt_attention_workspace_bytes (None when that is 0)."""
-    import torch
     w = "zdit_prompt_attention"
-    if any(t.dtype != torch.bfloat16 for t in (q, k, v, o)):
+    bf = _th().bfloat16
+    if not (q.dtype is bf and k.dtype is bf and v.dtype is bf and o.dtype is bf):
         raise ValueError(f"{w}: q, k, v and o must be bfloat16")
-    a = batch.args(q.shape[1], k.shape[1], q.shape[2], causal, scale)
-    a.q, a.k, a.v, a.o = _heads(w, "q", q), _heads(w, "k", k), _heads(w, "v", v, k.shape), _heads(w, "o", o)
-    if o.shape[1:] != q.shape[1:] or k.shape[2] != q.shape[2]:
-        raise ValueError(f"{w}: o must match q and k must match q's head_dim")
-    if q.shape[0] < batch.q_rows or o.shape[0] < batch.q_rows or k.shape[0] < batch.kv_rows:
+    (R, H, hd), (S, Hkv, _) = q.shape, k.shape
+    hq, ho = _heads(w, "q", q, (R, H, hd)), _heads(w, "o", o, (o.shape[0], H, hd))
+    hk, hv = _heads(w, "k", k, (S, Hkv, hd)), _heads(w, "v", v, (S, Hkv, hd))
+    if R < batch.q_rows or o.shape[0] < batch.q_rows or S < batch.kv_rows:
         raise ValueError(f"{w}: the batch needs {batch.q_rows} rows of q and o and {batch.kv_rows} of k and v")
     _on_device(w, q, k, v, o, workspace)
-    _check(lib().zdit_prompt_attention(C.byref(a), _ptr(workspace),
-                                       workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                       _stream(stream)), w)
+    a = batch.args(H, Hkv, hd, causal, scale, hq, hk, hv, ho)
+    pw, nw = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _check(lib().zdit_prompt_attention(C.byref(a), pw, nw, _stream(stream)), w)
 
 
 def zdit_linear(a, w, out, bias=None, act=ACT_NONE, residual=None, stream=None):
     """out [M, N] = residual + act(a [M, K] . w [N, K]^T + bias): a and w bf16, bias fp32,
     residual and out fp32 or bf16; residual may be out."""
-    import torch
     n = "zdit_linear"
-    M, K = a.shape
-    N = w.shape[0]
-    if a.dtype != torch.bfloat16 or w.dtype != torch.bfloat16 or w.dim() != 2 or w.shape[1] != K:
+    bf = _th().bfloat16
+    (M, K), (N, Kw) = a.shape, w.shape
+    if a.dtype is not bf or w.dtype is not bf or Kw != K:
         raise ValueError(f"{n}: a [M, K] and w [N, K] must be bfloat16 matrices with the same K")
-    for t in (out, residual):
-        if t is not None and (tuple(t.shape) != (M, N) or (N > 1 and t.stride(1) != 1)):
-            raise ValueError(f"{n}: out and residual must be [{M}, {N}] with contiguous rows")
-    if K > 1 and (a.stride(1) != 1 or w.stride(1) != 1):
+    (lda, ea), (ldw, ew), (ldo, eo) = a.stride(), w.stride(), out.stride()
+    if (ea != 1 or ew != 1) and K > 1:
         raise ValueError(f"{n}: rows of a and w must be contiguous")
-    _f32_vector(n, "bias", bias, N)
-    out_dtype, res_dtype = _dtype_code(out, n), 0 if residual is None else _dtype_code(residual, n)
+    if out.shape != (M, N) or (eo != 1 and N > 1):
+        raise ValueError(f"{n}: out must be [{M}, {N}] with contiguous rows")
+    pr, ldr, dr = None, 0, 0
+    if residual is not None:
+        (ldr, er), pr, dr = residual.stride(), residual.data_ptr(), _dtype_code(residual, n)
+        if residual.shape != (M, N) or (er != 1 and N > 1):
+            raise ValueError(f"{n}: residual must be [{M}, {N}] with contiguous rows")
+    g = LinearArgs(M, N, K, a.data_ptr(), lda, w.data_ptr(), ldw, _f32(n, "bias", bias, N), act, pr, ldr, dr,
+                   out.data_ptr(), ldo, _dtype_code(out, n))
     _on_device(n, a, w, out, bias, residual)
     if M == 0:
         return
-    g = LinearArgs(M=M, N=N, K=K, a=a.data_ptr(), lda=a.stride(0), w=w.data_ptr(), ldw=w.stride(0),
-                   bias=bias.data_ptr() if bias is not None else None, act=act, out=out.data_ptr(),
-                   ld_out=out.stride(0), out_dtype=out_dtype)
-    if residual is not None:
-        g.residual, g.ld_residual, g.residual_dtype = residual.data_ptr(), residual.stride(0), res_dtype
     _check(lib().zdit_linear(C.byref(g), _stream(stream)), n)
 
 

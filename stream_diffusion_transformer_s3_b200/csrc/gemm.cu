@@ -139,7 +139,7 @@ __device__ __forceinline__ void epilogue_tile(const KParams& p, uint32_t taddr, 
       float v[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-      linear_finish_row<32>(p.lin, row, col0, p.N, v);
+      linear_finish<32>(p.lin, row, col0, p.N, v);
     }
   } else if constexpr (EPI == EPI_SWIGLU) {
     // tile columns [0,128) hold gate rows 128*nb.., [128,256) the matching up rows

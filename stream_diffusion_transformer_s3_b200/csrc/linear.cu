@@ -1,9 +1,307 @@
 // zdit_linear: out = residual + act(a . w^T + bias).
+//
+// Two kernels.  Many rows: the persistent projection GEMM of gemm.cu with the epilogue of
+// linear_epi.cuh.  Few rows: the kernel below, which is bound by streaming w once.  There
+// the weights are the 128-row operand of the tensor core and the rows of a its N side (16 to
+// 256 columns, a multiple of 16), so a tile computes 128 output features for all rows with
+// no padding of M to 128, and N / 128 tiles times `split` parts of K spread the weights
+// over the SMs.  The parts of one tile are a cluster: each leaves its fp32 partial tile in
+// its own shared memory and every CTA adds up its share of the rows over the cluster's
+// shared memory, in rank order (the result does not depend on timing, and there is no
+// workspace to clear or share).
+//
+// Warp roles (320 threads): warp 0 loads (TMA ring), warp 1 issues the MMAs, warps 2-9 move
+// the accumulator (TMEM lane = feature, column = row of a) to shared memory and finish.
+#include <algorithm>
 #include <cmath>
 
 #include "internal.h"
 #include "linear_epi.cuh"
 #include "ptx.cuh"
+
+namespace zdit {
+
+bool make_tmap_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld_elems,
+                       uint32_t box_rows, uint32_t box_cols);
+
+namespace {
+
+constexpr int FT = 128;              // features per tile
+constexpr int BK = 64;               // K slice
+constexpr int W_TILE = FT * BK * 2;  // 16 KB
+constexpr int EPI_WARPS = 8;         // two per TMEM lane group
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int kMaxStages = 8;
+constexpr int kMaxSplit = 8;         // portable cluster size
+constexpr int kMaxRowTile = 160;     // rows of a in one tile
+
+struct FewParams {
+  int M, N;
+  int row_tile;  // rows of a per tile (UMMA N)
+  int slices;    // K slices in all
+  int split;     // CTAs per tile
+  int stages;
+  int group;     // K slices per ring stage
+  uint32_t tmem_cols;
+  LinearEpi e;
+  int* err;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t cta) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
+  return r;
+}
+
+__global__ void __launch_bounds__(THREADS)
+    linear_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
+                      const FewParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ uint64_t bars[2 * kMaxStages + 1];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = bars;
+  uint64_t* empty = bars + kMaxStages;
+  uint64_t* done = bars + 2 * kMaxStages;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int tile = blockIdx.x / p.split;
+  const int rank = blockIdx.x - tile * p.split;
+  const int f0 = tile * FT;
+  const int r0 = blockIdx.y * p.row_tile;
+  const int k_lo = (int)((int64_t)p.slices * rank / p.split), k_hi = (int)((int64_t)p.slices * (rank + 1) / p.split);
+  const int n = k_hi - k_lo;  // >= 1: split <= slices
+  const int slice_bytes = W_TILE + p.row_tile * BK * 2;
+  const int stage_bytes = p.group * slice_bytes;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmA);
+  }
+  if (warp == 1) tmem_alloc(&tmem_slot, p.tmem_cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  griddep_wait();
+  griddep_trigger();
+
+  if (warp == 0 && lane == 0) {
+    // (stage and phase are counted: a division by the run-time ring depth would cost more
+    // than the slice it serves)
+    int st = 0, k = k_lo * BK, left = n;
+    uint32_t phase = 0, armed = 0;
+    uint8_t* dst = smem;
+    while (left > 0) {
+      if (!mbar_wait(&empty[st], phase ^ 1, &abort_flag, p.err)) break;
+      const int g = min(p.group, left);
+      mbar_arrive_expect_tx(&full[st], g * slice_bytes);
+      for (int j = 0; j < g; ++j) tma_load_2d(dst + j * slice_bytes, &tmW, &full[st], k + j * BK, f0);
+      for (int j = 0; j < g; ++j) tma_load_2d(dst + j * slice_bytes + W_TILE, &tmA, &full[st], k + j * BK, r0);
+      armed = (armed & ~(1u << st)) | (phase << st) | (0x10000u << st);
+      left -= g;
+      k += g * BK;
+      dst += stage_bytes;
+      if (++st == p.stages) {
+        st = 0;
+        phase ^= 1;
+        dst = smem;
+      }
+    }
+    if (abort_flag) {  // let copies in flight land before shared memory is released
+      int dummy = 0;
+      for (int i = 0; i < p.stages; ++i)
+        if (armed & (0x10000u << i)) mbar_wait(&full[i], (armed >> i) & 1, &dummy);
+    }
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_bf16_f32(FT, p.row_tile);
+    const uint64_t w0 = sdesc_kmajor_sw128(smem_u32(smem));
+    const uint64_t stage_desc = stage_bytes >> 4, slice_desc = slice_bytes >> 4;  // linear in the address
+    int st = 0, left = n;
+    uint32_t phase = 0, acc = 0;
+    uint64_t ws = w0;
+    while (left > 0) {
+      if (!mbar_wait(&full[st], phase, &abort_flag, p.err)) break;
+      tc_fence_after();
+      const int g = min(p.group, left);
+      uint64_t w = ws;
+      for (int j = 0; j < g; ++j, w += slice_desc) {
+        const uint64_t a = w + (W_TILE >> 4);
+#pragma unroll
+        for (int k = 0; k < BK / 16; ++k) {
+          umma_bf16_ss(tmem, w + k * 2, a + k * 2, idesc, acc);
+          acc = 1u;
+        }
+      }
+      umma_commit(&empty[st]);
+      left -= g;
+      ws += stage_desc;
+      if (++st == p.stages) {
+        st = 0;
+        phase ^= 1;
+        ws = w0;
+      }
+    }
+    umma_commit(done);  // every MMA issued: the ring is idle once it fires
+    int dummy = 0;
+    mbar_wait(done, 0, &dummy);
+  }
+  __syncthreads();  // (the other warps wait here, not in a polling loop)
+  // The partial tile, [row][128 features] fp32, over the idle ring.
+  float* part = reinterpret_cast<float*>(smem);
+  const int rows = min(p.row_tile, p.M - r0);
+  if (warp >= 2) {
+    tc_fence_after();
+    if (!abort_flag) {
+      const int lg = warp & 3;
+      const uint32_t t0 = tmem + ((uint32_t)(lg * 32) << 16);
+      float* col = part + lg * 32 + lane;
+      for (int c = (warp - 2) / 4 * 16; c < rows; c += 32) {
+        uint32_t r[16];
+        tmem_ld16(t0 + c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) col[(c + j) * FT] = __uint_as_float(r[j]);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  cluster_sync();  // partial tiles of the whole cluster are visible
+  if (warp >= 2 && !abort_flag) {
+    // rows rank, rank + split, ... of the tile: a warp adds up kRows of them at a time, 4
+    // features per lane, all loads of the cluster in flight at once
+    const int f = f0 + lane * 4;
+    const uint32_t base = smem_u32(part) + lane * 16;
+    constexpr int kRows = 2;
+    const int step = EPI_WARPS * p.split;
+    uint32_t peer[kMaxSplit];
+#pragma unroll
+    for (int s = 0; s < kMaxSplit; ++s) peer[s] = map_cluster(base, s < p.split ? s : rank);
+    for (int r = rank + (warp - 2) * p.split; r < rows; r += kRows * step) {
+      float4 q[kRows][kMaxSplit];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+#pragma unroll
+        for (int s = 0; s < kMaxSplit; ++s)
+          q[i][s] = s < p.split && r + i * step < rows ? ld_cluster_f4(peer[s] + (r + i * step) * (FT * 4))
+                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        if (r + i * step >= rows) break;
+        float v[4] = {q[i][0].x, q[i][0].y, q[i][0].z, q[i][0].w};
+#pragma unroll
+        for (int s = 1; s < kMaxSplit; ++s) {
+          v[0] += q[i][s].x; v[1] += q[i][s].y; v[2] += q[i][s].z; v[3] += q[i][s].w;
+        }
+        linear_finish<4>(p.e, r0 + r + i * step, f, p.N, v);
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while a peer may still read its tile
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+}
+
+// How the few-row kernel covers a problem.
+struct FewPlan {
+  int row_tile, row_tiles, split, stages, group, smem;
+  uint32_t tmem_cols;
+};
+
+// Whether the few-row kernel takes a problem, and how.  us at N x K, M rows, this kernel
+// against the projection GEMM (bf16 out, SiLU, weights cold):
+//   2560 x 4096   M 16  8 / 31   M 133 16 / 32   M 512 20 / 27   M 1024 41 / 30
+//   9728 x 2560   M 16 13 / 24   M 133 19 / 25   M 200 29 / 25   M 512  57 / 35
+//   3840 x 10240  M 16 18 / 69   M 133 25 / 69   M 512 48 / 56   M 1024 86 / 62
+// i.e. up to 160 rows (one tile of them), and beyond that while the tiles alone (128 features
+// x up to 128 rows) do not give the GEMM's 256-wide tiles a GPU's worth of work.
+bool plan_few(int64_t M, int64_t N, int64_t K, FewPlan* f) {
+  const int64_t row_tiles = M <= kMaxRowTile ? 1 : (M + 127) / 128;
+  const int64_t tiles = (N + FT - 1) / FT * row_tiles;
+  const int sms = num_sms();
+  if (row_tiles > 1 && tiles * 5 > (int64_t)sms * 4) return false;
+  f->row_tiles = (int)row_tiles;
+  f->row_tile = (int)(((M + row_tiles - 1) / row_tiles + 15) / 16 * 16);
+  // Parts of K: about one CTA per SM; past half a GPU of tiles up to 1.6 per SM, because two
+  // CTAs on an SM hide each other's pipeline bubbles (9728 x 2560, 133 rows: 3 parts 18.9 us,
+  // 2 parts 21.5).  Clusters of 5 to 7 pack badly into the GPCs (6144 x 2560, 1 row: 6 parts
+  // 16.6 us, 3 parts 9.9).  At least 4 slices a part.
+  const int64_t slices = (K + BK - 1) / BK;
+  const int sizes[] = {8, 4, 3, 2, 1};
+  for (const int s : sizes) {
+    f->split = s;
+    if (s == 1) break;
+    if (slices / s < 4) continue;
+    if (tiles * s * 10 <= (int64_t)sms * 11) break;
+    if (tiles * 2 >= sms && tiles * s * 10 <= (int64_t)sms * 16 + 40) break;
+  }
+  // Two slices per stage while the rows are few (fewer waits: 1 row 7.9 -> 7.5 us); one when
+  // the row tile takes its share of the ring.  Two CTAs fit an SM.
+  f->group = f->row_tile <= 32 ? 2 : 1;
+  const int stage = f->group * (W_TILE + f->row_tile * BK * 2);
+  f->stages = std::min(110 * 1024 / stage, kMaxStages);
+  f->smem = 1024 + std::max(f->stages * stage, f->row_tile * FT * 4);
+  f->tmem_cols = 32;
+  while (f->tmem_cols < (uint32_t)f->row_tile) f->tmem_cols *= 2;
+  return true;
+}
+
+zdit_status launch_few(const zdit_linear_args& a, const LinearEpi& e, const FewPlan& f, cudaStream_t s) {
+  CUtensorMap tw, ta;
+  if (!make_tmap_bf16_2d(&tw, a.w, a.N, a.K, a.ldw, FT, BK) ||
+      !make_tmap_bf16_2d(&ta, a.a, a.M, a.K, a.lda, f.row_tile, BK))
+    return ZDIT_ERR_CUDA;
+  if (cudaFuncSetAttribute(linear_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem) != cudaSuccess)
+    return ZDIT_ERR_CUDA;
+  FewParams p;
+  p.M = (int)a.M; p.N = (int)a.N; p.row_tile = f.row_tile; p.slices = (int)((a.K + BK - 1) / BK); p.split = f.split;
+  p.stages = f.stages; p.group = f.group; p.tmem_cols = f.tmem_cols; p.e = e; p.err = device_error_ptr();
+  const double rw = (e.out_f32 ? 4.0 : 2.0) + (e.residual ? (e.res_f32 ? 4.0 : 2.0) : 0.0);
+  ProfScope ps(PROF_GEMM_OTHER, 2.0 * a.M * a.N * (double)a.K,
+               2.0 * ((double)a.M * a.K + (double)a.N * a.K) + rw * a.M * a.N, s);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.N + FT - 1) / FT * f.split), (unsigned)f.row_tiles);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = f.smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = f.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, linear_few_kernel, tw, ta, p) != cudaSuccess) return ZDIT_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? ZDIT_OK : ZDIT_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace zdit
 
 using namespace zdit;
 
@@ -27,14 +325,18 @@ ZDIT_API zdit_status zdit_linear(const zdit_linear_args* a, void* stream) {
     return ZDIT_ERR_ALIGNMENT;
   if ((reinterpret_cast<uintptr_t>(a->bias) & 3) || oa % oe || (a->residual && ra % re)) return ZDIT_ERR_ALIGNMENT;
   if (!device_ok()) return ZDIT_ERR_UNSUPPORTED;
+  LinearEpi e{};
+  e.bias = a->bias; e.residual = a->residual; e.out = a->out; e.ld_res = a->ld_residual; e.ld_out = a->ld_out;
+  e.act = a->act; e.res_f32 = re == 4; e.out_f32 = oe == 4;
+  e.vec = oa % 16 == 0 && a->ld_out * oe % 16 == 0 &&
+          (!a->residual || (ra % 16 == 0 && a->ld_residual * re % 16 == 0));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  FewPlan f;
+  if (plan_few(a->M, a->N, a->K, &f)) return launch_few(*a, e, f, s);
   GemmArgs g{};
   g.A = a->a; g.B = a->w; g.M = (int)a->M; g.N = (int)a->N; g.K = (int)a->K; g.lda = (int)a->lda; g.ldb = (int)a->ldw;
-  g.epi = EPI_LINEAR; g.out = a->out;
-  g.lin.bias = a->bias; g.lin.residual = a->residual; g.lin.out = a->out; g.lin.ld_res = a->ld_residual;
-  g.lin.ld_out = a->ld_out; g.lin.act = a->act; g.lin.res_f32 = re == 4; g.lin.out_f32 = oe == 4;
-  g.lin.vec = oa % 16 == 0 && a->ld_out * oe % 16 == 0 &&
-              (!a->residual || (ra % 16 == 0 && a->ld_residual * re % 16 == 0));
-  return launch_gemm(g, static_cast<cudaStream_t>(stream));
+  g.epi = EPI_LINEAR; g.out = a->out; g.lin = e;
+  return launch_gemm(g, s);
 }
 
 }  // extern "C"
