@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from dataclasses import dataclass, field
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -372,6 +373,21 @@ def zdit_device_status(stream=None):
 # ------------------------------------------------------------------------ prompt operators
 # These take torch tensors of any strides the C calls allow.  What the C structs cannot
 # carry (element types, shapes, the device) is checked here.
+def _packer(cls, fmt):
+    """Builds a `cls` from its values in one step (field-wise construction of nested
+    structures costs more than the launch of a small kernel)."""
+    s = struct.Struct(fmt)
+    assert s.size == C.sizeof(cls), (cls, s.size, C.sizeof(cls))
+    pack, make = s.pack, cls.from_buffer_copy
+    return lambda *v: make(pack(*v))
+
+
+_NO_HEADS = (0, 0, 0)
+_qk_args = _packer(QkNormRopeArgs, "@q5i4xPqqPqqPqqPqqPPf4xPPii")
+_attn_args = _packer(PromptAttentionArgs, "@i4xPPP4if4xPqqPqqPqqPqq")
+_linear_args = _packer(LinearArgs, "@qqqPqPqPi4xPqi4xPqi4x")
+
+
 def _dtype_code(t, where):
     T = _th()
     dt = t.dtype
@@ -390,22 +406,22 @@ def _on_device(where, *tensors):
 
 
 def _f32(where, name, t, *shape):
-    """Address of a contiguous fp32 tensor of that shape, None of None."""
+    """Address of a contiguous fp32 tensor of that shape, 0 of None."""
     if t is None:
-        return None
+        return 0
     if t.dtype is not _th().float32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be a contiguous float32 {list(shape)}")
     return t.data_ptr()
 
 
 def _heads(where, name, t, shape):
-    """Heads struct of a [rows, heads, head_dim] tensor whose last axis is contiguous."""
+    """Heads fields of a [rows, heads, head_dim] tensor whose last axis is contiguous."""
     if len(shape) != 3 or t.shape != shape:
         raise ValueError(f"{where}: {name} has shape {list(t.shape)}, expected [rows, heads, head_dim] = {list(shape)}")
     rs, hs, es = t.stride()
     if es != 1 and shape[2] > 1:
         raise ValueError(f"{where}: {name}'s last axis must be contiguous")
-    return Heads(t.data_ptr(), rs, hs)
+    return t.data_ptr(), rs, hs
 
 
 def zdit_rope_table_scaled(pos, rotary_dim, theta, cos_out, sin_out, scaling: RopeScaling = None, stream=None):
@@ -432,20 +448,20 @@ def zdit_qk_norm_rope(q, k, q_out, k_out, w_q, w_k, cos, sin, rotary_dim, layout
     hq, hqo = _heads(w, "q", q, (T, n_q, hd)), _heads(w, "q_out", q_out, (T, n_q, hd))
     if (k is None) != (k_out is None):
         raise ValueError(f"{w}: k and k_out go together")
-    n_k, hk, hko = 0, Heads(), Heads()
+    n_k, hk, hko = 0, _NO_HEADS, _NO_HEADS
     if k is not None:
         n_k = k.shape[1]
         if k.dtype is not q.dtype or k_out.dtype is not q_out.dtype:
             raise ValueError(f"{w}: k must have q's type and k_out q_out's")
         hk, hko = _heads(w, "k", k, (T, n_k, hd)), _heads(w, "k_out", k_out, (T, n_k, hd))
     pq, pk = _f32(w, "w_q", w_q, hd), _f32(w, "w_k", w_k, hd)
-    pc, ps = None, None
+    pc, ps = 0, 0
     if rotary_dim:
         if cos is None or sin is None:
             raise ValueError(f"{w}: a rotation needs cos and sin")
         pc, ps = _f32(w, "cos", cos, T, rotary_dim // 2), _f32(w, "sin", sin, T, rotary_dim // 2)
-    a = QkNormRopeArgs(T, n_q, n_k, hd, _dtype_code(q, w), _dtype_code(q_out, w), hq, hk, hqo, hko, pq, pk, eps, pc, ps,
-                       rotary_dim, layout)
+    a = _qk_args(T, n_q, n_k, hd, _dtype_code(q, w), _dtype_code(q_out, w), *hq, *hk, *hqo, *hko, pq, pk, eps, pc, ps,
+                 rotary_dim, layout)
     _on_device(w, q, k, q_out, k_out, w_q, w_k, cos, sin)
     if T == 0:
         return
@@ -464,14 +480,14 @@ class PromptBatch:
             raise ValueError("PromptBatch: q_len, kv_len and kv_start must have one entry per sequence")
         self.batch = n
         self.q_len, self.kv_len, self.kv_start = arr(q_len), arr(kv_len), arr(kv_start)
+        self._addr = tuple(0 if v is None else C.addressof(v) for v in (self.q_len, self.kv_len, self.kv_start))
         self.q_rows = sum(self.q_len)
         lens = list(self.q_len if kv_len is None else self.kv_len)
         ends = [s + m for s, m in zip(self.kv_start, lens)] if kv_start is not None else [sum(lens)]
         self.kv_rows = max(ends) if ends else 0
 
-    def args(self, n_heads, n_kv_heads, head_dim, causal, scale, *heads):
-        return PromptAttentionArgs(self.batch, self.q_len, self.kv_len, self.kv_start, n_heads, n_kv_heads, head_dim,
-                                   1 if causal else 0, scale, *heads)
+    def args(self, n_heads, n_kv_heads, head_dim, causal, scale, heads=_NO_HEADS * 4):
+        return _attn_args(self.batch, *self._addr, n_heads, n_kv_heads, head_dim, 1 if causal else 0, scale, *heads)
 
 
 def prompt_attention_workspace_bytes(batch: PromptBatch, n_heads, n_kv_heads, head_dim, causal=True) -> int:
@@ -493,7 +509,7 @@ def zdit_prompt_attention(q, k, v, o, batch: PromptBatch, workspace=None, causal
     if R < batch.q_rows or o.shape[0] < batch.q_rows or S < batch.kv_rows:
         raise ValueError(f"{w}: the batch needs {batch.q_rows} rows of q and o and {batch.kv_rows} of k and v")
     _on_device(w, q, k, v, o, workspace)
-    a = batch.args(H, Hkv, hd, causal, scale, hq, hk, hv, ho)
+    a = batch.args(H, Hkv, hd, causal, scale, hq + hk + hv + ho)
     pw, nw = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _check(lib().zdit_prompt_attention(C.byref(a), pw, nw, _stream(stream)), w)
 
@@ -511,13 +527,13 @@ def zdit_linear(a, w, out, bias=None, act=ACT_NONE, residual=None, stream=None):
         raise ValueError(f"{n}: rows of a and w must be contiguous")
     if out.shape != (M, N) or (eo != 1 and N > 1):
         raise ValueError(f"{n}: out must be [{M}, {N}] with contiguous rows")
-    pr, ldr, dr = None, 0, 0
+    pr, ldr, dr = 0, 0, 0
     if residual is not None:
         (ldr, er), pr, dr = residual.stride(), residual.data_ptr(), _dtype_code(residual, n)
         if residual.shape != (M, N) or (er != 1 and N > 1):
             raise ValueError(f"{n}: residual must be [{M}, {N}] with contiguous rows")
-    g = LinearArgs(M, N, K, a.data_ptr(), lda, w.data_ptr(), ldw, _f32(n, "bias", bias, N), act, pr, ldr, dr,
-                   out.data_ptr(), ldo, _dtype_code(out, n))
+    g = _linear_args(M, N, K, a.data_ptr(), lda, w.data_ptr(), ldw, _f32(n, "bias", bias, N), act, pr, ldr, dr,
+                     out.data_ptr(), ldo, _dtype_code(out, n))
     _on_device(n, a, w, out, bias, residual)
     if M == 0:
         return

@@ -8,30 +8,32 @@
 // are read once per key head, a single token fills `group` rows instead of one, and the mask
 // is a limit on the key index that depends on the row's token alone.
 //
-// One CTA = one item (sequence, key head, rows, range of 128-key tiles) with two softmax
-// slots of 128 threads, one thread per row:
-//   two query tiles  slots 0 and 1 take consecutive query tiles and the same key tiles
-//                    (arithmetic-bound: each K and V tile feeds 256 rows);
-//   one query tile   slots 0 and 1 take even and odd key tiles of the same rows and are
-//                    joined in shared memory (few rows: memory- and latency-bound, the
-//                    tensor core and softmax of one slot overlap the other's).
-// Warp roles (384 threads): warps 0-3 and 4-7 softmax of slots 0 and 1, warp 8 loads Q and
-// K, warp 9 issues the MMAs, warp 10 loads V (its own warp, so that a V stage still in use
-// never delays the next K), warp 11 completes the warpgroup that hands registers over
-// (168 per thread at launch -> 208 softmax, 88 control: 2 x 128 x 208 + 128 x 88 = 64512).
-// TMEM columns: S0 [0,128), S1 [128,256), O0 [256, +HD), O1 [384, +HD).  P (bf16 pairs) is
-// written over the first 64 columns of S and feeds the PV product from TMEM.
-// A slot's PV of its previous key tile is issued before its next S product, so the commit
-// that signals the new S also proves that PV done: the softmax may overwrite P and rescale O.
-// Softmax in fp32: running maximum that moves only when a row grows by more than 16 (log2
-// units; P <= 2^16 keeps bf16's relative precision), sum of the unrounded P in fp32.
+// Two kernels share that layout:
 //
-// Keys are split when the items would not fill the GPU: each part writes its normalised O
-// (fp32) with its maximum and sum to the workspace and a second kernel joins the parts of
-// a row in ascending order.
+// prompt_attn_wide: long prompts (arithmetic-bound).  One CTA per SM takes two query tiles
+//   and all their key tiles (128 keys), so that each K and V tile in shared memory feeds 256
+//   rows.  384 threads: warps 0-3 and 4-7 are the softmax of slots 0 and 1, one thread per
+//   row; warp 8 loads Q and K, warp 9 issues the MMAs, warp 10 loads V (its own warp, so that
+//   a V stage still in use never delays the next K), warp 11 completes the warpgroup that
+//   hands registers over (168 per thread at launch -> 208 softmax, 88 control: 2 x 128 x 208
+//   + 128 x 88 = 64512).  The last tile of an odd number has its even and odd key tiles on
+//   the two slots, joined in shared memory.
+// prompt_attn_narrow: short prompts, new rows after a prefix, single tokens (latency- and
+//   memory-bound).  One query tile per CTA, two CTAs per SM, so that one CTA's set-up, loads
+//   and output overlap the other's work; 64-key tiles with S double-buffered in TMEM, so that
+//   S of the next tile is ready when the softmax finishes the last one.  Keys are split over
+//   CTAs when the rows do not fill the GPU: each part writes its normalised O (fp32) with its
+//   maximum and sum to the workspace, and a third kernel joins the parts of a row in
+//   ascending order.
+//
+// In both, P (bf16 pairs) is written over the first columns of its S in TMEM and feeds the
+// PV product from there.  Softmax in fp32: a running maximum that moves only when a row grows
+// by more than 16 (log2 units; P <= 2^16 keeps bf16's relative precision), and the sum of the
+// unrounded P.
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <cstdlib>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -44,9 +46,12 @@ bool heads_disjoint(const zdit_heads& h, int64_t rows, int heads, int head_dim);
 
 namespace {
 
-constexpr int TILE = 128;  // rows of a query tile, keys of a key tile
-constexpr int THREADS = 384;
+constexpr int TILE = 128;       // rows of a query tile, keys of a key tile of the wide kernel
+constexpr int NTILE = 64;       // keys of a key tile of the narrow kernel
+constexpr int THREADS = 384;    // wide
 constexpr int WARP_QK = 8, WARP_MMA = 9, WARP_V = 10;
+constexpr int NTHREADS = 224;   // narrow: 4 softmax warps, Q and K, MMA, V
+constexpr int NWARP_QK = 4, NWARP_MMA = 5, NWARP_V = 6;
 constexpr int kMaxSeqs = 128;
 constexpr float kRescaleThreshold = 16.0f;  // log2 units
 
@@ -55,14 +60,14 @@ struct Plan {
   int n;  // sequences with query rows
   int item0[kMaxSeqs + 1];  // first item (per key head) of sequence i; item0[n] = all
   int q0[kMaxSeqs], q_len[kMaxSeqs], kv0[kMaxSeqs], kv_len[kMaxSeqs];
-  int parts[kMaxSeqs];      // key splits
+  int parts[kMaxSeqs];      // key splits (narrow kernel)
+  int chunk[kMaxSeqs];      // keys of a part, a multiple of NTILE
   int part0[kMaxSeqs];      // first partial row of the sequence in the workspace (parts > 1)
   int join0[kMaxSeqs + 1];  // first joined row (token, head) among sequences with parts > 1
 };
 
 struct PParams {
   int n_kv, group, tokens;  // tokens per query tile
-  int chunk;                // key tiles per part
   int causal;
   float scale_log2;
   __nv_bfloat16* o;
@@ -82,7 +87,6 @@ struct Cfg {
   static constexpr int OFF_V = OFF_K + ST * TILE_BYTES;
   static constexpr int OFF_BAR = OFF_V + ST * TILE_BYTES;
   static constexpr int SMEM = 1024 + OFF_BAR + 256;
-  static constexpr int STAGE_ROW = 2 * HD + 16;         // bf16 output row, padded against bank conflicts
   static constexpr int JOIN_ROW = HD + 4;               // fp32 row of slot 1 when slots are joined
 };
 
@@ -120,9 +124,112 @@ __device__ __forceinline__ int last_key(int tok, int q_len, int kv_len, int caus
   return causal ? min(tok + kv_len - q_len, kv_len - 1) : kv_len - 1;
 }
 
+// Item `item` (per key head): its sequence and its index inside the sequence.
+__device__ __forceinline__ int find_item(const Plan& plan, int item, int& rem) {
+  int lo = 0, hi = plan.n;  // plan.item0[lo] <= item < plan.item0[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (plan.item0[mid] <= item) lo = mid; else hi = mid;
+  }
+  rem = item - plan.item0[lo];
+  return lo;
+}
+
+// Running softmax of one row over a tile of N logits in s: moves the reference maximum if
+// needed (alpha then scales what was accumulated so far), replaces s by P = exp2(s scale -
+// m_ref) packed as bf16 pairs in pk and returns the sum of the unrounded P.
+template <int N>
+__device__ __forceinline__ float row_max(const float (&s)[N]) {
+  float m8[8];  // independent chains of 3-input max
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m8[e] = fmaxf(s[e], s[8 + e]);
+#pragma unroll
+  for (int e = 16; e < N; e += 16)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m8[k] = fmax3(m8[k], s[e + k], s[e + 8 + k]);
+  return fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], fmax3(m8[5], m8[6], m8[7])));
+}
+
+template <int N>
+__device__ __forceinline__ float row_exp(const float (&s)[N], float scale_log2, float m_use, uint32_t tS) {
+  const uint64_t sc2 = pk2(scale_log2, scale_log2);
+  const uint64_t nm2 = pk2(-m_use, -m_use);
+  uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+  for (int e4 = 0; e4 < N / 32; ++e4) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint64_t x2 = fma2(pk2(s[e4 * 32 + 2 * e], s[e4 * 32 + 2 * e + 1]), sc2, nm2);
+      float a, b;
+      unpk2(x2, a, b);
+      const float p0 = ex2(a), p1 = ex2(b);
+      sum4[e & 3] = add2(sum4[e & 3], pk2(p0, p1));
+      pk[e] = pack_bf16x2(p0, p1);
+    }
+    tmem_st16(tS + e4 * 16, pk);
+  }
+  float a0, a1, a2, a3, a4, a5, a6, a7;
+  unpk2(sum4[0], a0, a1);
+  unpk2(sum4[1], a2, a3);
+  unpk2(sum4[2], a4, a5);
+  unpk2(sum4[3], a6, a7);
+  return ((a0 + a1) + (a2 + a3)) + ((a4 + a5) + (a6 + a7));
+}
+
+// O (HD columns of TMEM) *= alpha.
+template <int HD>
+__device__ __forceinline__ void scale_o(uint32_t tO, float alpha) {
+#pragma unroll 1
+  for (int e = 0; e < HD / 16; ++e) {
+    uint32_t r[16];
+    tmem_ld16(tO + e * 16, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha);
+    tmem_st16(tO + e * 16, r);
+  }
+}
+
+// Keys past the end of the sequence have P = 0, but 0 times whatever those rows of V hold
+// need not be 0: row `row` of a V tile in shared memory is cleared.
+template <int HD>
+__device__ __forceinline__ void clear_v_row(uint8_t* v_tile, int half_bytes, int row) {
+  for (int h = 0; h < HD / 64; ++h)
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      *reinterpret_cast<uint4*>(v_tile + h * half_bytes + row * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// One warp's 32 finished rows as bf16, staged in shared memory (row pitch padded against
+// bank conflicts) and stored as whole rows; off: element offset of this lane's row in o, -1
+// for none.  take(e4, v) yields 32 columns of the row.
+template <int HD, typename Take>
+__device__ __forceinline__ void store_rows(uint8_t* stage, int lane, long long off, __nv_bfloat16* o, Take take) {
+  constexpr int PITCH = 2 * HD + 16;
+  for (int e4 = 0; e4 < HD / 32; ++e4) {
+    float v[32];
+    take(e4, v);
+    uint4* dst = reinterpret_cast<uint4*>(stage + lane * PITCH + e4 * 64);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      dst[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                          pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+  }
+  __syncwarp();
+  constexpr int LPR = HD / 8;  // lanes per row
+#pragma unroll 4
+  for (int it = 0; it < LPR; ++it) {
+    const int r = it * (32 / LPR) + lane / LPR;
+    const long long ro = __shfl_sync(0xffffffffu, off, r);
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * PITCH + (lane % LPR) * 16);
+    if (ro >= 0) *reinterpret_cast<uint4*>(o + ro + (lane % LPR) * 8) = v;
+  }
+}
+
 template <int HD>
 __global__ void __launch_bounds__(THREADS, 1)
-    prompt_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+    prompt_attn_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Plan plan, const PParams p) {
   using C = Cfg<HD>;
   constexpr int ST = C::ST;
@@ -149,27 +256,16 @@ __global__ void __launch_bounds__(THREADS, 1)
   // item of this CTA: key heads fastest, so that all heavy items come first
   const int item = blockIdx.x / p.n_kv;
   const int kvh = blockIdx.x - item * p.n_kv;
-  int lo = 0, hi = plan.n;  // plan.item0[lo] <= item < plan.item0[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (plan.item0[mid] <= item) lo = mid; else hi = mid;
-  }
-  const int sq = lo;
+  int rem;
+  const int sq = find_item(plan, item, rem);
   const int q_len = plan.q_len[sq], kv_len = plan.kv_len[sq], kv0 = plan.kv0[sq], q0 = plan.q0[sq];
-  const int parts = plan.parts[sq];
-  const int rem = item - plan.item0[sq];
   const int n_pairs = (q_len + 2 * p.tokens - 1) / (2 * p.tokens);
-  const int part = rem % parts;
-  const int pair = n_pairs - 1 - rem / parts;  // later rows see more keys: first
-  const int tok0 = pair * 2 * p.tokens;
-  const bool two = tok0 + p.tokens < q_len;    // two query tiles, or one with split keys
-  const int first_tile = part * p.chunk;
-  // key tiles [first_tile, first_tile + n) of this item; slot 0 of two stops after n0
+  const int tok0 = (n_pairs - 1 - rem) * 2 * p.tokens;  // later rows see more keys: first
+  const bool two = tok0 + p.tokens < q_len;             // two query tiles, or one with split keys
+  // key tiles [0, n) of this item; slot 0 of two stops after n0
   auto tiles_for = [&](int tok_end) {
     const int lk = last_key(min(tok_end, q_len) - 1, q_len, kv_len, p.causal);
-    int t = lk < 0 ? 0 : lk / TILE + 1;
-    if (parts > 1) t = min(t, first_tile + p.chunk);
-    return max(t - first_tile, 0);
+    return lk < 0 ? 0 : lk / TILE + 1;
   };
   const int n0 = tiles_for(tok0 + p.tokens);
   const int n = two ? tiles_for(tok0 + 2 * p.tokens) : n0;
@@ -221,7 +317,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint8_t* sK = smem + C::OFF_K + st * C::TILE_BYTES;
         mbar_arrive_expect_tx(&k_full[st], C::TILE_BYTES);
         for (int c = 0; c < HD / 64; ++c)
-          tma_load_3d(sK + c * C::HALF, &tmK, &k_full[st], c * 64, kvh, kv0 + (first_tile + i) * TILE);
+          tma_load_3d(sK + c * C::HALF, &tmK, &k_full[st], c * 64, kvh, kv0 + i * TILE);
         ++issued;
         if (i == 0 && two) load_q(1);
       }
@@ -240,7 +336,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint8_t* sV = smem + C::OFF_V + st * C::TILE_BYTES;
         mbar_arrive_expect_tx(&v_full[st], C::TILE_BYTES);
         for (int c = 0; c < HD / 64; ++c)
-          tma_load_3d(sV + c * C::HALF, &tmV, &v_full[st], c * 64, kvh, kv0 + (first_tile + i) * TILE);
+          tma_load_3d(sV + c * C::HALF, &tmV, &v_full[st], c * 64, kvh, kv0 + i * TILE);
         ++issued;
       }
       if (*abort_flag) {
@@ -334,21 +430,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (int c = 0; c < cnt; ++c) {
       const int i = two ? c : 2 * c + t;
-      const int key0 = (first_tile + i) * TILE;
+      const int key0 = i * TILE;
       ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], c & 1, abort_flag, p.err));
       if (!ok) break;
       tc_fence_after();
       if (key0 + TILE > kv_len && (!two || t == 0 || i >= n0)) {
-        // keys past the end of the sequence: their P is 0, but 0 times whatever the rows of
-        // V there hold need not be, so the rows are cleared (by the slot that uses them first)
+        // (by the slot that uses the tile first)
         ok = __all_sync(0xffffffffu, mbar_wait(&v_full[i % ST], (i / ST) & 1, abort_flag, p.err));
         if (!ok) break;
-        if (row >= kv_len - key0) {
-          uint8_t* sV = smem + C::OFF_V + (i % ST) * C::TILE_BYTES + row * 128;
-          for (int h = 0; h < HD / 64; ++h)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(sV + h * C::HALF + e * 16) = make_uint4(0, 0, 0, 0);
-        }
+        if (row >= kv_len - key0) clear_v_row<HD>(smem + C::OFF_V + (i % ST) * C::TILE_BYTES, C::HALF, row);
         fence_proxy_async_smem();
       }
       if (warp_live) {
@@ -367,16 +457,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int e = 0; e < TILE; ++e)
             if (e > valid) s[e] = -INFINITY;
         }
-        // row max: 8 independent chains of 3-input max
-        float m8[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m8[e] = fmaxf(s[e], s[8 + e]);
-#pragma unroll
-        for (int e = 16; e < TILE; e += 16)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) m8[k] = fmax3(m8[k], s[e + k], s[e + 8 + k]);
-        float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], fmax3(m8[5], m8[6], m8[7])));
-        mx *= p.scale_log2;
+        const float mx = row_max<TILE>(s) * p.scale_log2;
         float alpha = 1.f;
         bool move = false;
         if (c == 0) {
@@ -386,43 +467,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           m_ref = mx;
           move = true;
         }
-        l_sum *= alpha;
-        if (__any_sync(0xffffffffu, move)) {  // O is stable: the previous PV completed before this S
-#pragma unroll 1
-          for (int e = 0; e < HD / 16; ++e) {
-            uint32_t r[16];
-            tmem_ld16(tO + e * 16, r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha);
-            tmem_st16(tO + e * 16, r);
-          }
-        }
-        // P = exp2(s scale - m_ref); a row with no key yet has m_ref = -inf: use 0, P = 0
-        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-        const uint64_t sc2 = pk2(p.scale_log2, p.scale_log2);
-        const uint64_t nm2 = pk2(-m_use, -m_use);
-        uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int e4 = 0; e4 < 4; ++e4) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint64_t x2 = fma2(pk2(s[e4 * 32 + 2 * e], s[e4 * 32 + 2 * e + 1]), sc2, nm2);
-            float a, b;
-            unpk2(x2, a, b);
-            const float p0 = ex2(a), p1 = ex2(b);
-            sum4[e & 3] = add2(sum4[e & 3], pk2(p0, p1));
-            pk[e] = pack_bf16x2(p0, p1);
-          }
-          tmem_st16(tS + e4 * 16, pk);
-        }
-        float a0, a1, a2, a3, a4, a5, a6, a7;
-        unpk2(sum4[0], a0, a1);
-        unpk2(sum4[1], a2, a3);
-        unpk2(sum4[2], a4, a5);
-        unpk2(sum4[3], a6, a7);
-        l_sum += ((a0 + a1) + (a2 + a3)) + ((a4 + a5) + (a6 + a7));
+        // O is stable: the previous PV completed before this S
+        if (__any_sync(0xffffffffu, move)) scale_o<HD>(tO, alpha);
+        // (a row with no key yet has m_ref = -inf: with 0 in its place P is 0)
+        l_sum = l_sum * alpha + row_exp<TILE>(s, p.scale_log2, m_ref == -INFINITY ? 0.f : m_ref, tS);
         tmem_st_wait();
       }
       tc_fence_before();
@@ -493,45 +541,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int e = 0; e < 32; ++e) v[e] = 0.f;
         }
       };
-      if (parts > 1) {
-        if (warp_live) {
-          const int64_t at = (int64_t)plan.part0[sq] +
-                             ((int64_t)part * q_len + tok) * (p.n_kv * p.group) + head;
-          if (live) p.part_ml[at] = make_float2(m_ref, l_sum);
-          for (int e4 = 0; e4 < HD / 32; ++e4) {
-            float v[32];
-            take(e4, v);
-            if (live) {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + e4 * 32);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-            }
-            __syncwarp();
-          }
-        }
-      } else if (warp_live) {
-        // bf16 rows staged in the idle Q and K space of this slot, stored as whole rows
-        uint8_t* stage = smem + C::OFF_Q + t * (C::OFF_V / 2) + lg * 32 * C::STAGE_ROW;
-        for (int e4 = 0; e4 < HD / 32; ++e4) {
-          float v[32];
-          take(e4, v);
-          uint4* dst = reinterpret_cast<uint4*>(stage + lane * C::STAGE_ROW + e4 * 64);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
-                                pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
-        }
-        __syncwarp();
-        const long long off = live ? (q0 + (int64_t)tok) * p.o_rs + head * p.o_hs : -1;
-        constexpr int LPR = HD / 8;  // lanes per row
-#pragma unroll 4
-        for (int it = 0; it < LPR; ++it) {
-          const int r = it * (32 / LPR) + lane / LPR;
-          const long long ro = __shfl_sync(0xffffffffu, off, r);
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * C::STAGE_ROW + (lane % LPR) * 16);
-          if (ro >= 0) *reinterpret_cast<uint4*>(p.o + ro + (lane % LPR) * 8) = v;
-        }
-      }
+      if (warp_live)  // staged in the idle Q and K space of this slot
+        store_rows<HD>(smem + C::OFF_Q + t * (C::OFF_V / 2) + lg * 32 * (2 * HD + 16), lane,
+                       live ? (q0 + (int64_t)tok) * p.o_rs + head * p.o_hs : -1, p.o, take);
     }
     tc_fence_before();
   }
@@ -539,6 +551,286 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == WARP_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HD>
+struct NCfg {
+  static constexpr int Q_HALF = TILE * 128;              // 64 columns x 128 rows
+  static constexpr int Q_BYTES = (HD / 64) * Q_HALF;
+  static constexpr int HALF = NTILE * 128;               // 64 columns x 64 keys, 8 KB
+  static constexpr int TILE_BYTES = (HD / 64) * HALF;
+  static constexpr int ST = HD == 128 ? 2 : 4;           // ring depth of K and of V (32 KB each)
+  static constexpr int OFF_K = Q_BYTES;
+  static constexpr int OFF_V = OFF_K + ST * TILE_BYTES;
+  static constexpr int OFF_BAR = OFF_V + ST * TILE_BYTES;
+  static constexpr int SMEM = 1024 + OFF_BAR + 256;      // two CTAs fit an SM
+};
+
+// TMEM columns: S buffers [0,64) and [64,128), O [128, +HD); 256 per CTA.
+template <int HD>
+__global__ void __launch_bounds__(NTHREADS, 2)
+    prompt_attn_narrow_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Plan plan,
+                              const PParams p) {
+  using C = NCfg<HD>;
+  constexpr int ST = C::ST;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_full = bars;
+  uint64_t* pv_done = bars + 1;     // one phase per PV product
+  uint64_t* mma_done = bars + 2;
+  uint64_t* s_full = bars + 3;      // [2]
+  uint64_t* p_full = bars + 5;      // [2]
+  uint64_t* k_full = bars + 7;      // [ST]
+  uint64_t* k_empty = k_full + ST;  // [ST]
+  uint64_t* v_full = k_empty + ST;  // [ST]
+  uint64_t* v_empty = v_full + ST;  // [ST]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_empty + ST);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(pv_done, 1);
+    mbar_init(mma_done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+    }
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == NWARP_QK && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+  }
+  if (warp == NWARP_V && lane == 0) tma_prefetch_desc(&tmV);
+  if (warp == NWARP_MMA) tmem_alloc(tmem_slot, 256);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int item = blockIdx.x / p.n_kv;
+  const int kvh = blockIdx.x - item * p.n_kv;
+  int rem;
+  const int sq = find_item(plan, item, rem);
+  const int q_len = plan.q_len[sq], kv_len = plan.kv_len[sq], kv0 = plan.kv0[sq], q0 = plan.q0[sq];
+  const int parts = plan.parts[sq], chunk = plan.chunk[sq];
+  const int n_tiles = (q_len + p.tokens - 1) / p.tokens;
+  const int part = rem % parts;
+  const int tok0 = (n_tiles - 1 - rem / parts) * p.tokens;  // later rows see more keys: first
+  const int key_first = part * chunk;
+  int n;  // key tiles of this item
+  {
+    const int lk = last_key(min(tok0 + p.tokens, q_len) - 1, q_len, kv_len, p.causal);
+    const int end = parts > 1 ? min(lk + 1, key_first + chunk) : lk + 1;
+    n = end > key_first ? (end - key_first + NTILE - 1) / NTILE : 0;
+  }
+  griddep_wait();     // Q, K, V of the predecessor are complete, the workspace is free
+  griddep_trigger();  // every CTA has started: the successor may launch
+
+  if (warp == NWARP_QK) {
+    if (lane == 0 && n > 0) {
+      // ------------------------------------------------------------ Q and K
+      mbar_arrive_expect_tx(q_full, (uint32_t)(p.group * p.tokens * 128 * (HD / 64)));
+      for (int c = 0; c < HD / 64; ++c)
+        tma_load_3d(smem + c * C::Q_HALF, &tmQ, q_full, c * 64, kvh * p.group, q0 + tok0);
+      int issued = 0;
+      for (int i = 0; i < n; ++i) {
+        const int st = i % ST;
+        if (!mbar_wait(&k_empty[st], ((i / ST) & 1) ^ 1, abort_flag, p.err)) break;
+        uint8_t* sK = smem + C::OFF_K + st * C::TILE_BYTES;
+        mbar_arrive_expect_tx(&k_full[st], C::TILE_BYTES);
+        for (int c = 0; c < HD / 64; ++c)
+          tma_load_3d(sK + c * C::HALF, &tmK, &k_full[st], c * 64, kvh, kv0 + key_first + i * NTILE);
+        ++issued;
+      }
+      if (*abort_flag) {  // let copies in flight land before shared memory is released
+        int dummy = 0;
+        mbar_wait(q_full, 0, &dummy);
+        for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(&k_full[i % ST], (i / ST) & 1, &dummy);
+      }
+    }
+  } else if (warp == NWARP_V) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ V
+      int issued = 0;
+      for (int i = 0; i < n; ++i) {
+        const int st = i % ST;
+        if (!mbar_wait(&v_empty[st], ((i / ST) & 1) ^ 1, abort_flag, p.err)) break;
+        uint8_t* sV = smem + C::OFF_V + st * C::TILE_BYTES;
+        mbar_arrive_expect_tx(&v_full[st], C::TILE_BYTES);
+        for (int c = 0; c < HD / 64; ++c)
+          tma_load_3d(sV + c * C::HALF, &tmV, &v_full[st], c * 64, kvh, kv0 + key_first + i * NTILE);
+        ++issued;
+      }
+      if (*abort_flag) {
+        int dummy = 0;
+        for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(&v_full[i % ST], (i / ST) & 1, &dummy);
+      }
+    }
+  } else if (warp == NWARP_MMA) {
+    if (lane == 0 && n > 0) {
+      // ------------------------------------------------------------ MMA issuer
+      const uint32_t id_s = idesc_bf16_f32(TILE, NTILE);            // Q, K both K-major
+      const uint32_t id_o = idesc_bf16_f32(TILE, HD, false, true);  // P from TMEM, V MN-major
+      const uint64_t dq = sdesc_kmajor_sw128(smem_u32(smem));
+      const uint64_t dk = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_K));
+      const uint64_t dv = sdesc_mnmajor_sw128(smem_u32(smem + C::OFF_V), C::HALF, 1024);
+      constexpr uint64_t kTileDesc = C::TILE_BYTES >> 4;
+      bool ok = mbar_wait(q_full, 0, abort_flag, p.err);
+      // S_i into buffer i & 1: after PV of tile i - 2, which read P from the same columns
+      auto sk = [&](int i) -> bool {
+        if (!mbar_wait(&k_full[i % ST], (i / ST) & 1, abort_flag, p.err)) return false;
+        tc_fence_after();
+        const uint64_t kb = dk + (i % ST) * kTileDesc;
+        const uint32_t d = tmem + (i & 1) * NTILE;
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k)
+          umma_bf16_ss(d, dq + (uint64_t)(((k >> 2) * C::Q_HALF + (k & 3) * 32) >> 4),
+                       kb + (uint64_t)(((k >> 2) * C::HALF + (k & 3) * 32) >> 4), id_s, k != 0 ? 1u : 0u);
+        umma_commit(&s_full[i & 1]);
+        umma_commit(&k_empty[i % ST]);
+        return true;
+      };
+      if (ok) ok = sk(0);
+      if (ok && n > 1) ok = sk(1);
+      for (int i = 0; ok && i < n; ++i) {
+        if (!(ok = mbar_wait(&p_full[i & 1], (i >> 1) & 1, abort_flag, p.err))) break;
+        if (!(ok = mbar_wait(&v_full[i % ST], (i / ST) & 1, abort_flag, p.err))) break;
+        tc_fence_after();
+        const uint64_t vb = dv + (i % ST) * kTileDesc;
+        const uint32_t pa = tmem + (i & 1) * NTILE;
+#pragma unroll
+        for (int k = 0; k < NTILE / 16; ++k)
+          umma_bf16_ts(tmem + 2 * NTILE, pa + k * 8, vb + (uint64_t)((k * 16 * 128) >> 4), id_o, (i | k) != 0 ? 1u : 0u);
+        umma_commit(pv_done);
+        umma_commit(&v_empty[i % ST]);
+        if (i + 2 < n) ok = sk(i + 2);
+      }
+      umma_commit(mma_done);
+      int dummy = 0;
+      mbar_wait(mma_done, 0, &dummy);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int row = warp * 32 + lane;
+    const int tok = tok0 + row / p.group;
+    const int head = kvh * p.group + row % p.group;
+    const bool live = row < p.group * p.tokens && tok < q_len;
+    const bool warp_live = __any_sync(0xffffffffu, live);
+    const int lim = live ? last_key(tok, q_len, kv_len, p.causal) : kv_len - 1;
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const uint32_t tO = tmem + lane_off + 2 * NTILE;
+    float m_ref = -INFINITY, l_sum = 0.f;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int key0 = key_first + i * NTILE;
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i & 1], (i >> 1) & 1, abort_flag, p.err));
+      if (!ok) break;
+      tc_fence_after();
+      if (key0 + NTILE > kv_len) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&v_full[i % ST], (i / ST) & 1, abort_flag, p.err));
+        if (!ok) break;
+        if (row < NTILE && row >= kv_len - key0)
+          clear_v_row<HD>(smem + C::OFF_V + (i % ST) * C::TILE_BYTES, C::HALF, row);
+        fence_proxy_async_smem();
+      }
+      if (warp_live) {
+        const uint32_t tS = tmem + lane_off + (i & 1) * NTILE;
+        float s[NTILE];
+#pragma unroll
+        for (int e4 = 0; e4 < NTILE / 32; ++e4) {
+          uint32_t r[32];
+          tmem_ld32(tS + e4 * 32, r);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) s[e4 * 32 + e] = __uint_as_float(r[e]);
+        }
+        tmem_ld_wait();
+        const int valid = lim - key0;  // last allowed column of this tile
+        if (valid < NTILE - 1) {
+#pragma unroll
+          for (int e = 0; e < NTILE; ++e)
+            if (e > valid) s[e] = -INFINITY;
+        }
+        const float mx = row_max<NTILE>(s) * p.scale_log2;
+        float alpha = 1.f;
+        bool move = false;
+        if (i == 0) {
+          m_ref = mx;
+        } else if (mx > m_ref + kRescaleThreshold) {
+          alpha = ex2(m_ref - mx);
+          m_ref = mx;
+          move = true;
+        }
+        if (__any_sync(0xffffffffu, move)) {
+          // the previous PV may still be adding to O (phase i - 1; the one before it completed
+          // before this S, which was issued after it)
+          ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (i - 1) & 1, abort_flag, p.err));
+          if (!ok) break;
+          tc_fence_after();
+          scale_o<HD>(tO, alpha);
+        }
+        l_sum = l_sum * alpha + row_exp<NTILE>(s, p.scale_log2, m_ref == -INFINITY ? 0.f : m_ref, tS);
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[i & 1]);
+    }
+    // ------------------------------------------------------------ epilogue
+    // (pv_done could be two phases behind here, which its parity does not show)
+    if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(mma_done, 0, abort_flag, p.err));
+    tc_fence_after();
+    if (ok && warp_live) {
+      const float inv = l_sum == 0.f ? 0.f : 1.0f / l_sum;
+      auto take = [&](int e4, float (&v)[32]) {  // 32 columns of the finished row
+        if (n > 0) {
+          uint32_t r[32];
+          tmem_ld32(tO + e4 * 32, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]) * inv;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0.f;
+        }
+      };
+      if (parts > 1) {
+        const int64_t at = (int64_t)plan.part0[sq] + ((int64_t)part * q_len + tok) * (p.n_kv * p.group) + head;
+        if (live) p.part_ml[at] = make_float2(m_ref, l_sum);
+        for (int e4 = 0; e4 < HD / 32; ++e4) {
+          float v[32];
+          take(e4, v);
+          if (live) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + e4 * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
+          __syncwarp();
+        }
+      } else {
+        // every product is done: Q and the rings are idle
+        store_rows<HD>(smem + warp * 32 * (2 * HD + 16), lane,
+                       live ? (q0 + (int64_t)tok) * p.o_rs + head * p.o_hs : -1, p.o, take);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == NWARP_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
   }
 }
 
@@ -597,17 +889,57 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
     *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
 }
 
+constexpr int kMinPart = 256;  // keys of a part at least
+
+// Whether the wide kernel takes a call (see the table at make_plan).
+bool use_wide(int64_t ctas, int64_t keys_per_tile, int64_t sms) {
+  static const int f = getenv("ZDIT_WIDE") ? atoi(getenv("ZDIT_WIDE")) : -1;
+  if (f >= 0) return f;
+  return ctas >= sms && keys_per_tile >= 1024;
+}
+
+// Keys of a part: the length that gives the earliest end when the parts run over two slots
+// per SM, a part costing its keys plus kPartCost.
+template <typename Seq>
+int64_t choose_part(const Seq* seq, int n, int tokens, int n_kv, int64_t sms) {
+  constexpr int64_t kPartCost = 512;
+  const int64_t slots = 2 * sms;
+  int64_t longest = 1, items = 0, keys = 0;
+  for (int i = 0; i < n; ++i) {
+    const int64_t t = (int64_t)((seq[i].ql + tokens - 1) / tokens) * n_kv;
+    longest = std::max<int64_t>(longest, seq[i].kl);
+    items += t;
+    keys += t * seq[i].kl;
+  }
+  if (items >= slots || longest <= 2 * kMinPart) return INT_MAX;
+  int64_t best = INT_MAX, best_cost = longest + kPartCost / 2;  // not split: no join either
+  for (int c = kMinPart; c < longest; c += c / 4 / NTILE * NTILE) {
+    int64_t m = 0;
+    int big = 0;
+    for (int i = 0; i < n; ++i) {
+      const int parts = std::max(1, (seq[i].kl + c - 1) / c);
+      m += (int64_t)((seq[i].ql + tokens - 1) / tokens) * n_kv * parts;
+      big = std::max(big, (seq[i].kl + parts - 1) / parts);
+    }
+    const int64_t waves = (m + slots - 1) / slots;
+    const int64_t cost = std::max(waves * (big + kPartCost), (keys + m * kPartCost) / slots + kPartCost);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = c;
+    }
+  }
+  return best;
+}
+
 struct HostPlan {
   Plan p;
-  int tokens, group, chunk;
+  bool wide;
+  int tokens, group;
   int64_t q_rows, kv_rows, part_rows;
   double pairs;  // allowed (query, key) pairs, for the profiler
 };
 
-constexpr int kMinChunk = 4;   // key tiles of a part at least
-constexpr int kSplitGain = 2;  // split only what is this many chunks long
-
-// Items, splits and workspace rows of a call; false on invalid lengths.
+// Kernel, items, splits and workspace rows of a call; false on invalid lengths.
 bool make_plan(const zdit_prompt_attention_args& a, HostPlan* h) {
   if (a.batch <= 0 || a.batch > kMaxSeqs || !a.q_len || a.n_kv_heads <= 0 || a.n_heads <= 0 ||
       a.n_heads % a.n_kv_heads || a.n_heads / a.n_kv_heads > 64 || (a.head_dim != 64 && a.head_dim != 128) ||
@@ -615,47 +947,50 @@ bool make_plan(const zdit_prompt_attention_args& a, HostPlan* h) {
     return false;
   h->group = a.n_heads / a.n_kv_heads;
   h->tokens = TILE / h->group;
-  struct Seq { int q0, ql, kv0, kl, tiles; };
+  struct Seq { int q0, ql, kv0, kl; };
   Seq seq[kMaxSeqs];
   int n = 0;
-  int64_t q = 0, kv = 0, work = 0;
+  int64_t q = 0, kv = 0;
+  int64_t work = 0;   // keys over all one-tile items of a key head
+  int64_t tiles = 0;  // one-tile items of a key head
+  int64_t pairs = 0;  // two-tile items of a key head
   h->kv_rows = 0;
   h->pairs = 0;
-  int longest = 0;
   for (int b = 0; b < a.batch; ++b) {
     const int64_t ql = a.q_len[b], kl = a.kv_len ? a.kv_len[b] : ql, k0 = a.kv_start ? a.kv_start[b] : kv;
     if (ql < 0 || kl < 0 || k0 < 0 || k0 + kl > (1 << 30) || q + ql > (1 << 30)) return false;
     if (!a.kv_start) kv += kl;
     h->kv_rows = std::max(h->kv_rows, k0 + kl);
     if (ql > 0) {
-      seq[n++] = Seq{(int)q, (int)ql, (int)k0, (int)kl, (int)((kl + TILE - 1) / TILE)};
-      const int64_t tiles = (kl + TILE - 1) / TILE, pairs = (ql + 2 * h->tokens - 1) / (2 * h->tokens);
-      work += tiles * pairs;  // (an upper bound for causal rows)
-      longest = std::max(longest, (int)tiles);
-      const double full = (double)ql * kl;
-      if (!a.causal) h->pairs += full;
-      else if (kl >= ql) h->pairs += full - 0.5 * ql * (ql - 1.0);
-      else h->pairs += 0.5 * kl * (kl + 1.0);
+      seq[n++] = Seq{(int)q, (int)ql, (int)k0, (int)kl};
+      double seen = (double)ql * kl;  // allowed pairs
+      if (a.causal) seen = kl >= ql ? seen - 0.5 * ql * (ql - 1.0) : 0.5 * kl * (kl + 1.0);
+      h->pairs += seen;
+      tiles += (ql + h->tokens - 1) / h->tokens;
+      pairs += (ql + 2 * h->tokens - 1) / (2 * h->tokens);
+      work += (int64_t)(seen / h->tokens) + 1;
     }
     q += ql;
   }
   h->q_rows = q;
-  const int64_t ideal = (work * a.n_kv_heads + num_sms() - 1) / num_sms();
-  h->chunk = (int)std::max<int64_t>(ideal, kMinChunk);
-  if (longest <= kSplitGain * h->chunk) h->chunk = std::max(longest, 1);
-  std::sort(seq, seq + n, [](const Seq& x, const Seq& y) { return x.tiles != y.tiles ? x.tiles > y.tiles : x.q0 < y.q0; });
+  const int64_t sms = num_sms();
+  h->wide = use_wide(pairs * a.n_kv_heads, n > 0 ? work / std::max<int64_t>(tiles, 1) : 0, sms);
+  // Longest key range first: its items start early.
+  std::sort(seq, seq + n, [](const Seq& x, const Seq& y) { return x.kl != y.kl ? x.kl > y.kl : x.q0 < y.q0; });
+  const int64_t part_keys = h->wide ? INT_MAX : choose_part(seq, n, h->tokens, a.n_kv_heads, sms);
   int64_t items = 0, parts_rows = 0, join = 0;
   Plan& p = h->p;
   p.n = n;
   for (int i = 0; i < n; ++i) {
     const Seq& s = seq[i];
-    const int64_t pairs = (s.ql + 2 * h->tokens - 1) / (2 * h->tokens);
-    const int parts = std::max(1, (s.tiles + h->chunk - 1) / h->chunk);
+    const int per = h->wide ? 2 * h->tokens : h->tokens;
+    const int parts = (int)std::max<int64_t>(1, (s.kl + part_keys - 1) / part_keys);
     p.item0[i] = (int)items;
     p.q0[i] = s.q0; p.q_len[i] = s.ql; p.kv0[i] = s.kv0; p.kv_len[i] = s.kl; p.parts[i] = parts;
+    p.chunk[i] = ((s.kl + parts - 1) / parts + NTILE - 1) / NTILE * NTILE;  // parts of equal length
     p.part0[i] = (int)parts_rows;
     p.join0[i] = (int)join;
-    items += pairs * parts;
+    items += (int64_t)((s.ql + per - 1) / per) * parts;
     if (parts > 1) {
       join += (int64_t)s.ql * a.n_heads;
       parts_rows += (int64_t)s.ql * a.n_heads * parts;
@@ -677,17 +1012,24 @@ size_t plan_bytes(const HostPlan& h, int head_dim) {
 template <int HD>
 zdit_status launch_prompt(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const HostPlan& h,
                           const PParams& p, cudaStream_t s) {
-  using C = Cfg<HD>;
-  // per launch: the opt-in belongs to the current context
-  if (cudaFuncSetAttribute(prompt_attn_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-    return ZDIT_ERR_CUDA;
   const int H = p.n_kv * p.group;
   {
     ProfScope ps(PROF_ATTENTION, 4.0 * HD * H * h.pairs,
                  2.0 * HD * (2.0 * H * h.q_rows + 2.0 * p.n_kv * h.kv_rows), s);
-    if (launch_dependent(prompt_attn_kernel<HD>, dim3((unsigned)(h.p.item0[h.p.n] * p.n_kv)), dim3(THREADS), C::SMEM, s,
-                         tq, tk, tv, h.p, p) != cudaSuccess)
+    const dim3 grid((unsigned)(h.p.item0[h.p.n] * p.n_kv));
+    // the shared-memory opt-in is set per launch: it belongs to the current context
+    if (h.wide) {
+      if (cudaFuncSetAttribute(prompt_attn_wide_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Cfg<HD>::SMEM) != cudaSuccess ||
+          launch_dependent(prompt_attn_wide_kernel<HD>, grid, dim3(THREADS), Cfg<HD>::SMEM, s, tq, tk, tv, h.p, p) !=
+              cudaSuccess)
+        return ZDIT_ERR_CUDA;
+    } else if (cudaFuncSetAttribute(prompt_attn_narrow_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    NCfg<HD>::SMEM) != cudaSuccess ||
+               launch_dependent(prompt_attn_narrow_kernel<HD>, grid, dim3(NTHREADS), NCfg<HD>::SMEM, s, tq, tk, tv, h.p,
+                                p) != cudaSuccess) {
       return ZDIT_ERR_CUDA;
+    }
   }
   const int join = h.p.join0[h.p.n];
   if (join > 0) {
@@ -742,7 +1084,7 @@ ZDIT_API zdit_status zdit_prompt_attention(const zdit_prompt_attention_args* a, 
   if (h.q_rows == 0) return ZDIT_OK;
   if (!device_ok()) return ZDIT_ERR_UNSUPPORTED;
   PParams p;
-  p.n_kv = a->n_kv_heads; p.group = h.group; p.tokens = h.tokens; p.chunk = h.chunk; p.causal = a->causal;
+  p.n_kv = a->n_kv_heads; p.group = h.group; p.tokens = h.tokens; p.causal = a->causal;
   const float scale = a->scale == 0.f ? 1.0f / sqrtf((float)a->head_dim) : a->scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.o = static_cast<__nv_bfloat16*>(a->o.ptr); p.o_rs = a->o.row_stride; p.o_hs = a->o.head_stride;
@@ -751,14 +1093,16 @@ ZDIT_API zdit_status zdit_prompt_attention(const zdit_prompt_attention_args* a, 
                                              ((size_t)h.part_rows * sizeof(float2) + 255) / 256 * 256) : nullptr;
   p.err = device_error_ptr();
   CUtensorMap tq, tk, tv;
+  const int key_box = h.wide ? TILE : NTILE;
   if (h.kv_rows == 0) {
     // no sequence has a key: no K or V tile is loaded, the maps only have to be valid
-    if (!make_tmap_bf16_heads(&tk, a->q.ptr, 1, 1, a->head_dim, a->head_dim, a->head_dim, 1, TILE)) return ZDIT_ERR_CUDA;
+    if (!make_tmap_bf16_heads(&tk, a->q.ptr, 1, 1, a->head_dim, a->head_dim, a->head_dim, 1, key_box))
+      return ZDIT_ERR_CUDA;
     tv = tk;
   } else if (!make_tmap_bf16_heads(&tk, a->k.ptr, h.kv_rows, a->n_kv_heads, a->head_dim, a->k.row_stride,
-                                   a->k.head_stride, 1, TILE) ||
+                                   a->k.head_stride, 1, key_box) ||
              !make_tmap_bf16_heads(&tv, a->v.ptr, h.kv_rows, a->n_kv_heads, a->head_dim, a->v.row_stride,
-                                   a->v.head_stride, 1, TILE)) {
+                                   a->v.head_stride, 1, key_box)) {
     return ZDIT_ERR_CUDA;
   }
   if (!make_tmap_bf16_heads(&tq, a->q.ptr, h.q_rows, a->n_heads, a->head_dim, a->q.row_stride, a->q.head_stride,

@@ -220,6 +220,12 @@ def attention_ref(q, k, v, q_len, kv_len, kv_start, causal, scale):
     return O, B
 
 
+def workspace(batch, H, Hkv, hd, causal=True):
+    """What the call needs, every byte set so that a value read before it is written is NaN."""
+    need = Z.prompt_attention_workspace_bytes(batch, H, Hkv, hd, causal)
+    return torch.full((need,), 255, dtype=torch.uint8, device="cuda") if need else None
+
+
 def run_attention(q_len, kv_len=None, kv_start=None, H=8, Hkv=2, hd=128, causal=True, seed=0, scale=0.0, gap=0,
                   qscale=1.0, head_major=False, label=""):
     """One call on inputs with NaN in every row of k and v that no sequence owns and a
@@ -242,12 +248,11 @@ def run_attention(q_len, kv_len=None, kv_start=None, H=8, Hkv=2, hd=128, causal=
     if head_major:
         o = o.transpose(0, 1).contiguous().transpose(0, 1)
     batch = Z.PromptBatch(q_len, kv_len, kv_start)
-    need = Z.prompt_attention_workspace_bytes(batch, H, Hkv, hd, causal)
-    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda") if need else None  # NaN patterns
+    ws = workspace(batch, H, Hkv, hd, causal)
     Z.zdit_prompt_attention(q, k, v, o, batch, ws, causal=causal, scale=scale)
     sc = scale if scale else hd ** -0.5
     ref, bound = attention_ref(q[:T], k, v, q_len, lens, starts, causal, sc)
-    check(o[:T], ref, bound, label or f"attention q {q_len} kv {lens} {H}/{Hkv}x{hd} split {need > 0}")
+    check(o[:T], ref, bound, label or f"attention q {q_len} kv {lens} {H}/{Hkv}x{hd} split {ws is not None}")
     assert (o[T:] == 17.0).all()
     return o, (q, k, v, batch, ws)
 
@@ -315,8 +320,7 @@ def test_prompt_attention_reference_maximum_moves():
         for rows in (n, 1):
             o = torch.empty(rows, H, hd, device="cuda", dtype=torch.bfloat16)
             b = Z.PromptBatch([rows], [n])
-            Z.zdit_prompt_attention(q[:rows], k, v, o, b, None if rows > 1 else torch.empty(
-                Z.prompt_attention_workspace_bytes(b, H, H, hd), dtype=torch.uint8, device="cuda"))
+            Z.zdit_prompt_attention(q[:rows], k, v, o, b, workspace(b, H, H, hd))
             ref, bound = attention_ref(q[:rows], k, v, [rows], [n], [0], True, hd ** -0.5)
             check(o, ref, bound, f"moving maximum {sign} {rows}")
 
@@ -330,7 +334,8 @@ def test_prompt_attention_equals_joint_attention_without_mask():
     T = sum(lengths)
     q, k, v = (rnd(i, T, H, 128) for i in (1, 2, 3))
     a, b = torch.empty_like(q), torch.empty_like(q)
-    Z.zdit_prompt_attention(q, k, v, a, Z.PromptBatch(lengths), causal=False)
+    batch = Z.PromptBatch(lengths)
+    Z.zdit_prompt_attention(q, k, v, a, batch, workspace(batch, H, H, 128, False), causal=False)
     Z.zdit_joint_attention(q.view(T, -1), k.view(T, -1), v.view(T, -1), b.view(T, -1), Z.DeviceVarlen([0, 130, T]), H)
     ref, bound = attention_ref(q, k, v, lengths, lengths, (0, 130), False, 128 ** -0.5)
     check(a, ref, bound, "unmasked")
@@ -373,8 +378,7 @@ def test_prompt_attention_far_row_offsets():
     q = rnd(3, 40, 2, hd)
     o = torch.empty_like(q)
     b = Z.PromptBatch([40], [900], [start])
-    ws = torch.empty(Z.prompt_attention_workspace_bytes(b, 2, 1, hd), dtype=torch.uint8, device="cuda")
-    Z.zdit_prompt_attention(q, k, v, o, b, ws)
+    Z.zdit_prompt_attention(q, k, v, o, b, workspace(b, 2, 1, hd))
     ref, bound = attention_ref(q, k[start:], v[start:], [40], [900], [0], True, hd ** -0.5)
     check(o, ref, bound, "far rows")
 
@@ -499,13 +503,14 @@ class Layer:
     def run(self, x, x16, pos, q_len, out, buf):
         H, Hkv, hd = self.H, self.Hkv, self.hd
         T = x.shape[0]
-        qkv, cos, sin, o = buf
+        qkv, cos, sin, o, ws = buf
         Z.zdit_rope_table_scaled(pos, hd, 1e6, cos, sin)
         Z.zdit_linear(x16, self.w_qkv, qkv)
         q, k, v = (qkv[:, a:b].view(T, -1, hd) for a, b in ((0, H * hd), (H * hd, (H + Hkv) * hd),
                                                             ((H + Hkv) * hd, (H + 2 * Hkv) * hd)))
         Z.zdit_qk_norm_rope(q, k, q, k, self.nq, self.nk, cos, sin, hd, Z.ROPE_HALF)
-        Z.zdit_prompt_attention(q, k, v, o, Z.PromptBatch(q_len))
+        batch = Z.PromptBatch(q_len)
+        Z.zdit_prompt_attention(q, k, v, o, batch, ws)
         Z.zdit_linear(o.view(T, -1), self.w_o, out, residual=x)
 
 
@@ -518,7 +523,8 @@ def test_prompt_layer_feeds_the_image_model(q_len):
     pos = torch.cat([torch.arange(n) for n in q_len]).to(device="cuda", dtype=torch.int32)
     out = torch.empty_like(x)
     buf = (torch.empty(T, 8 * 64, device="cuda", dtype=torch.bfloat16), torch.empty(T, 32, device="cuda"),
-           torch.empty(T, 32, device="cuda"), torch.empty(T, 4, 64, device="cuda", dtype=torch.bfloat16))
+           torch.empty(T, 32, device="cuda"), torch.empty(T, 4, 64, device="cuda", dtype=torch.bfloat16),
+           workspace(Z.PromptBatch(q_len), 4, 2, 64))
     L.run(x, x16, pos, q_len, out, buf)
     assert Z.zdit_device_status() == 0
     ref = L.exact(x, pos, q_len)
@@ -566,14 +572,13 @@ def test_prompt_rows_of_a_later_call_match_the_whole_prompt():
     H, Hkv, hd, n = 8, 2, 128, 400
     q, k, v = rnd(1, n, H, hd), rnd(2, n, Hkv, hd), rnd(3, n, Hkv, hd)
     whole = torch.empty_like(q)
-    Z.zdit_prompt_attention(q, k, v, whole, Z.PromptBatch([n]))
+    b = Z.PromptBatch([n])
+    Z.zdit_prompt_attention(q, k, v, whole, b, workspace(b, H, Hkv, hd))
     parts = torch.empty_like(q)
     at = 0
     for m in (250, 147, 1, 1, 1):
         b = Z.PromptBatch([m], [at + m])
-        need = Z.prompt_attention_workspace_bytes(b, H, Hkv, hd)
-        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
-        Z.zdit_prompt_attention(q[at:at + m], k, v, parts[at:at + m], b, ws)
+        Z.zdit_prompt_attention(q[at:at + m], k, v, parts[at:at + m], b, workspace(b, H, Hkv, hd))
         at += m
     ref, bound = attention_ref(q, k, v, [n], [n], [0], True, hd ** -0.5)
     check(whole, ref, bound, "whole")
