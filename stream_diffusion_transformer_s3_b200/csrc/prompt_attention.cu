@@ -835,58 +835,92 @@ __global__ void __launch_bounds__(NTHREADS, 2)
 }
 
 // Joins the parts of a split row: O = sum_s w_s O_s / sum_s w_s, w_s = l_s 2^(m_s - max m).
-// One warp per (token, head) row, parts in ascending order.
+// One CTA per (token, head) row; warp w takes the parts w, w + 4, ..., the warps' sums are
+// added in order (the result does not depend on timing).  A chain of dependent loads, so
+// everything that does not come from the parts is found before the wait, and the partial
+// rows are requested together with their maxima.
+constexpr int kJoinWarps = 4;
 template <int HD>
-__global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ Plan plan, const PParams p) {
-  griddep_wait();
-  griddep_trigger();
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (r >= plan.join0[plan.n]) return;
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    prompt_join_kernel(const __grid_constant__ Plan plan, const PParams p) {
+  constexpr int V = HD / 32, AHEAD = 4;
+  __shared__ float sh[kJoinWarps][HD + 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = blockIdx.x;
   int lo = 0, hi = plan.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (plan.join0[mid] <= r) lo = mid; else hi = mid;
   }
   const int H = p.n_kv * p.group;
-  const int rows = plan.q_len[lo] * H, parts = plan.parts[lo];
+  const int64_t rows = (int64_t)plan.q_len[lo] * H;
+  const int parts = plan.parts[lo];
   const int rr = r - plan.join0[lo];
   const int64_t at = (int64_t)plan.part0[lo] + rr;
-  float m = -INFINITY;
-  for (int s = lane; s < parts; s += 32) {
-    const float2 ml = p.part_ml[at + (int64_t)s * rows];
-    if (ml.y != 0.f) m = fmaxf(m, ml.x);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  constexpr int V = HD / 32;
-  float acc[V] = {};
-  float den = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < parts; ++s) {
-    const float2 ml = p.part_ml[at + (int64_t)s * rows];
-    float v[V];
-    const float* src = p.part_o + (at + (int64_t)s * rows) * HD + lane * V;
-    if constexpr (V == 4) {
-      const float4 f = *reinterpret_cast<const float4*>(src);
-      v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-    } else {
-      const float2 f = *reinterpret_cast<const float2*>(src);
-      v[0] = f.x; v[1] = f.y;
-    }
-    const float w = ml.y == 0.f ? 0.f : ml.y * ex2(ml.x - m);
-    den += w;
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = fmaf(w, v[e], acc[e]);
-  }
-  const float inv = den == 0.f ? 0.f : 1.0f / den;
   const int tok = rr / H, head = rr - tok * H;
-  __nv_bfloat16* dst = p.o + (plan.q0[lo] + (int64_t)tok) * p.o_rs + head * p.o_hs + lane * V;
-  if constexpr (V == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
-                                                pack_bf16x2(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  __nv_bfloat16* dst = p.o + (plan.q0[lo] + (int64_t)tok) * p.o_rs + head * p.o_hs;
+  griddep_wait();
+  griddep_trigger();
+  // this warp's parts, AHEAD at a time, each with a running maximum
+  float m = -INFINITY, den = 0.f, acc[V] = {};
+  for (int s0 = warp; s0 < parts; s0 += AHEAD * kJoinWarps) {
+    float2 ml[AHEAD];
+    float v[AHEAD][V];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const int s = s0 + j * kJoinWarps;
+      ml[j] = make_float2(-INFINITY, 0.f);
+      if (s < parts) {
+        const int64_t a = at + s * rows;
+        ml[j] = p.part_ml[a];
+        const float* src = p.part_o + a * HD + lane * V;
+        if constexpr (V == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(src);
+          v[j][0] = f.x; v[j][1] = f.y; v[j][2] = f.z; v[j][3] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(src);
+          v[j][0] = f.x; v[j][1] = f.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      if (ml[j].y == 0.f) continue;  // no key of this part is allowed for the row
+      const float mn = fmaxf(m, ml[j].x);
+      const float f = m == -INFINITY ? 0.f : ex2(m - mn), w = ml[j].y * ex2(ml[j].x - mn);
+      den = den * f + w;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(w, v[j][e], acc[e] * f);
+      m = mn;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) sh[warp][lane * V + e] = acc[e];
+  if (lane == 0) {
+    sh[warp][HD] = m;
+    sh[warp][HD + 1] = den;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    float mm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) mm = sh[w][HD + 1] == 0.f ? mm : fmaxf(mm, sh[w][HD]);
+    float d = 0.f, o[V] = {};
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      if (sh[w][HD + 1] == 0.f) continue;
+      const float f = ex2(sh[w][HD] - mm);
+      d = fmaf(sh[w][HD + 1], f, d);
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = fmaf(sh[w][lane * V + e], f, o[e]);
+    }
+    const float inv = d == 0.f ? 0.f : 1.0f / d;
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(dst + lane * V) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv),
+                                                             pack_bf16x2(o[2] * inv, o[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(dst + lane * V) = pack_bf16x2(o[0] * inv, o[1] * inv);
+  }
 }
 
 constexpr int kMinPart = 256;  // keys of a part at least
@@ -1034,7 +1068,8 @@ zdit_status launch_prompt(const CUtensorMap& tq, const CUtensorMap& tk, const CU
   const int join = h.p.join0[h.p.n];
   if (join > 0) {
     ProfScope ps(PROF_ATTENTION, 0.0, (4.0 * HD + 8.0) * h.part_rows + 2.0 * HD * join, s);
-    if (launch_dependent(prompt_join_kernel<HD>, dim3((unsigned)((join + 3) / 4)), dim3(128), 0, s, h.p, p) !=
+    if (launch_dependent(prompt_join_kernel<HD>, dim3((unsigned)join), dim3(32 * kJoinWarps), 0, s,
+                         h.p, p) !=
         cudaSuccess)
       return ZDIT_ERR_CUDA;
   }

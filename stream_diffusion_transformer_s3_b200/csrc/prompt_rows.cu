@@ -19,20 +19,18 @@ struct RopeScaledParams {
   const int* pos;
   int64_t T;
   int pairs;
-  double theta, factor, original_len, beta_fast, beta_slow;
+  double log2_base;  // w_i = 2^(-2i/d log2_base) before LINEAR / YARN scaling
+  double factor, original_len, beta_fast, beta_slow;
   int kind;
   float magnitude;
   float* cs;
   float* sn;
 };
 
+// (exp2 of a product instead of a power: its relative error grows with the exponent, but
+// pos * w carries it times w log2(1/w) <= 0.54, so the angle is as good: |pos| 2^-53.)
 __device__ double scaled_frequency(const RopeScaledParams& p, int i) {
-  const double d = 2.0 * p.pairs;
-  if (p.kind == ZDIT_ROPE_SCALE_NTK) {
-    const double base = p.theta * pow(p.factor, d / (d - 2.0));
-    return pow(base, -2.0 * i / d);
-  }
-  const double w = pow(p.theta, -2.0 * i / d);
+  const double w = exp2(-(double)i / p.pairs * p.log2_base);
   if (p.kind == ZDIT_ROPE_SCALE_LINEAR) return w / p.factor;
   if (p.kind == ZDIT_ROPE_SCALE_YARN) {
     const double turns = p.original_len * w * 0.15915494309189535;  // 1 / 2 pi
@@ -46,19 +44,28 @@ __device__ double scaled_frequency(const RopeScaledParams& p, int i) {
 // n of pi/2 in double with pi/2 split in two parts (Cody and Waite): n < 2^31 * 2/pi * w_0,
 // and the second part carries the product to ~2^-75 of n, so the remainder is good to
 // |angle| 2^-53.  The remainder (|r| <= pi/4) is rounded to fp32, an error of at most
-// 2^-25 absolute, below the half step 2^-25 of outputs in [1/2, 1]; then the fp32 sine and
-// cosine.  A double sincos costs ~40 FP64 operations per element, this ~5.
+// 2^-25 absolute, below the half step 2^-25 of outputs in [1/2, 1]; then the Taylor series
+// of sine and cosine to r^9 and r^10 (first terms left out: r^11/11! < 1.8e-9 and r^12/12!
+// < 1.2e-10).  About 30 instructions an element; a double sincos takes ~40 FP64 operations.
 __device__ __forceinline__ void sincos_of(double x, float& s, float& c) {
   const double n = rint(x * 0.63661977236758134);
-  double r = fma(-n, 1.5707963267948966, x);
-  r = fma(-n, 6.123233995736766e-17, r);
-  float sr, cr;
-  sincosf((float)r, &sr, &cr);
-  const int q = (int)((long long)n & 3);
-  s = (q & 1) ? cr : sr;
-  c = (q & 1) ? sr : cr;
-  if (q & 2) s = -s;
-  if (q == 1 || q == 2) c = -c;
+  double rd = fma(-n, 1.5707963267948966, x);
+  rd = fma(-n, 6.123233995736766e-17, rd);
+  const float r = (float)rd, q = r * r;
+  float ps = fmaf(q, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  ps = fmaf(q, ps, 1.0f / 120.0f);
+  ps = fmaf(q, ps, -1.0f / 6.0f);
+  const float sr = fmaf(r * q, ps, r);
+  float pc = fmaf(q, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+  pc = fmaf(q, pc, -1.0f / 720.0f);
+  pc = fmaf(q, pc, 1.0f / 24.0f);
+  pc = fmaf(q, pc, -0.5f);
+  const float cr = fmaf(q, pc, 1.0f);
+  const int k = (int)((long long)n & 3);  // quadrant
+  s = (k & 1) ? cr : sr;
+  c = (k & 1) ? sr : cr;
+  if (k & 2) s = -s;
+  if ((k + 1) & 2) c = -c;
 }
 
 // A row of `pairs` values per token, VEC consecutive ones per thread, `tpr` threads per row
@@ -99,7 +106,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scaled_kernel(const RopeSca
 constexpr int kQkThreads = 256;
 
 struct QkParams {
-  int64_t units;  // T * (n_q + n_k)
+  int64_t T;
+  int tokens;  // tokens per CTA
   int n_q, n_k, head_dim, pairs;
   const void *q, *k;
   void *qo, *ko;
@@ -109,21 +117,11 @@ struct QkParams {
   int in_f32, out_f32;
 };
 
-__device__ __forceinline__ void load8(const void* base, int64_t at, bool f32, float (&v)[8]) {
-  if (f32) {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = s[0], b = s[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
+__device__ __forceinline__ void load8_f32(const float* p, float (&v)[8]) {
+  const float4* s = reinterpret_cast<const float4*>(p);
+  const float4 a = s[0], b = s[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
 __device__ __forceinline__ void store8(void* base, int64_t at, bool f32, const float (&v)[8]) {
@@ -137,123 +135,234 @@ __device__ __forceinline__ void store8(void* base, int64_t at, bool f32, const f
   }
 }
 
-// A group of G lanes (a power of two >= head_dim / 8) holds one head, 8 elements a lane,
-// so each head is read and written once in 16-byte accesses and its sum of squares is a
-// shuffle reduction.  HALF pairs (i, i + pairs): when pairs is a multiple of 8 the partner
-// elements are one other lane's (shuffles); otherwise they go through shared memory (MODE
-// 2).  Interleaved pairs are a lane's own (MODE 0).
-enum { PAIR_OWN = 0, PAIR_SHUFFLE = 1, PAIR_SHARED = 2 };
+// A group of G lanes takes one head of `tokens` consecutive tokens.  Lane l holds two chunks
+// of 8 elements, at 8 l and at 8 (C + l), C = ceil(head_dim / 16) <= G: each head is read and
+// written once in 16-byte accesses, its sum of squares is a shuffle reduction, and the pairs
+// (i, i + head_dim / 2) of a wholly rotated head are a lane's own.  Neighbouring groups take
+// neighbouring heads, so a CTA reads whole stretches of a row.
+// The kernel is bound by instructions before it is bound by memory.  16381 x 40 heads of
+// 128, bf16, a quarter rotated: 87 us with 8 elements a lane and the head and token of every
+// 16 bytes found by division, 80 us with each group staying on its head (norm weights in
+// registers, addresses advancing by a row), 69 us with 16 elements a lane (two
+// tokens in flight per lane: 73 us, four: 103 us, their registers cost more threads).
+enum {
+  PAIR_OWN = 0,     // interleaved: pairs inside a chunk
+  PAIR_LOCAL = 1,   // halves of the whole head: element i of both chunks
+  PAIR_SHUFFLE = 2, // halves inside the first chunks: another lane's elements
+  PAIR_SHARED = 3   // any other split: through shared memory
+};
+// The rotation tables of one lane and token: 4 or 8 pairs, and (PAIR_OWN) 4 more for the
+// second chunk.
+template <int N>
+__device__ __forceinline__ void load_pairs(const float* cs, const float* sn, int i0, int pairs, bool vec, float (&c)[N],
+                                           float (&s)[N]) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 c4 = *reinterpret_cast<const float4*>(cs + i0 + i), s4 = *reinterpret_cast<const float4*>(sn + i0 + i);
+      c[i] = c4.x; c[i + 1] = c4.y; c[i + 2] = c4.z; c[i + 3] = c4.w;
+      s[i] = s4.x; s[i + 1] = s4.y; s[i + 2] = s4.z; s[i + 3] = s4.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool in = i0 + i < pairs;
+      c[i] = in ? cs[i0 + i] : 1.f;
+      s[i] = in ? sn[i0 + i] : 0.f;
+    }
+  }
+}
 
-template <int G, int MODE>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkParams p) {
-  __shared__ float xs[MODE == PAIR_SHARED ? kQkThreads * 8 : 1];
-  griddep_wait();
-  griddep_trigger();
-  const int lane = threadIdx.x & (G - 1);
-  const int64_t unit = (int64_t)blockIdx.x * (kQkThreads / G) + threadIdx.x / G;
-  const int heads = p.n_q + p.n_k;
-  const bool live = unit < p.units && lane * 8 < p.head_dim;
-  const int64_t t = unit / heads;
-  int h = (int)(unit - t * heads);
-  const bool is_q = h < p.n_q;
-  if (!is_q) h -= p.n_q;
-  const int e0 = lane * 8;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (live) {
-    if (is_q)
-      load8(p.q, t * p.q_rs + h * p.q_hs + e0, p.in_f32, v);
-    else
-      load8(p.k, t * p.k_rs + h * p.k_hs + e0, p.in_f32, v);
+__device__ __forceinline__ void rotate_own(float (&v)[8], const float (&c)[4], const float (&s)[4], int i0, int pairs) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x = v[2 * i], y = v[2 * i + 1];
+    if (i0 + i < pairs) {
+      v[2 * i] = x * c[i] - y * s[i];
+      v[2 * i + 1] = x * s[i] + y * c[i];
+    }
   }
-  const float* w = is_q ? p.w_q : p.w_k;
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-#pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (w != nullptr && live) {
-    const float r = 1.0f / sqrtf(fmaf(ss, p.inv_dim, p.eps));
-    float wv[8];
-    load8(w, e0, true, wv);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * r * wv[i];
+}
+
+template <bool F32>
+struct RawChunk {
+  uint4 u[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const char* p, bool live) {
+    u[0] = make_uint4(0, 0, 0, 0);
+    if constexpr (F32) u[1] = make_uint4(0, 0, 0, 0);
+    if (live) {
+      u[0] = reinterpret_cast<const uint4*>(p)[0];
+      if constexpr (F32) u[1] = reinterpret_cast<const uint4*>(p)[1];
+    }
   }
-  if (p.pairs > 0) {
-    const float* cs = p.cos + t * p.pairs;
-    const float* sn = p.sin + t * p.pairs;
-    if constexpr (MODE == PAIR_OWN) {
-      const int i0 = e0 / 2;
-      if (live && i0 < p.pairs) {
-        float c[4], s[4];
-        if ((p.pairs & 3) == 0) {
-          const float4 c4 = *reinterpret_cast<const float4*>(cs + i0), s4 = *reinterpret_cast<const float4*>(sn + i0);
-          c[0] = c4.x; c[1] = c4.y; c[2] = c4.z; c[3] = c4.w;
-          s[0] = s4.x; s[1] = s4.y; s[2] = s4.z; s[3] = s4.w;
-        } else {
+  __device__ __forceinline__ void unpack(float (&v)[8]) const {
+    const uint32_t a[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+    if constexpr (F32) {
+      const uint32_t b[4] = {u[1].x, u[1].y, u[1].z, u[1].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool in = i0 + i < p.pairs;
-            c[i] = in ? cs[i0 + i] : 1.f;
-            s[i] = in ? sn[i0 + i] : 0.f;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = v[2 * i], b = v[2 * i + 1];
-          if (i0 + i < p.pairs) {
-            v[2 * i] = a * c[i] - b * s[i];
-            v[2 * i + 1] = a * s[i] + b * c[i];
-          }
-        }
-      }
-    } else if constexpr (MODE == PAIR_SHUFFLE) {
-      const int step = p.pairs / 8;  // lanes between partners
-      const bool lo = lane < step, hi = !lo && lane < 2 * step;
-      const int src = lo ? lane + step : (hi ? lane - step : lane);
-      float o[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, v[i], src, G);
-      if (live && (lo || hi)) {
-        const int i0 = lo ? e0 : e0 - p.pairs;
-        float c[8], s[8];
-        load8(cs, i0, true, c);
-        load8(sn, i0, true, s);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = lo ? v[i] * c[i] - o[i] * s[i] : o[i] * s[i] + v[i] * c[i];
+      for (int i = 0; i < 4; ++i) {
+        v[i] = __uint_as_float(a[i]);
+        v[4 + i] = __uint_as_float(b[i]);
       }
     } else {
-      float* x = xs + (threadIdx.x / G) * (G * 8);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[e0 + i] = v[i];
-      __syncwarp();
-      if (live) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = e0 + i;
-          if (e < p.pairs)
-            v[i] = v[i] * cs[e] - x[e + p.pairs] * sn[e];
-          else if (e < 2 * p.pairs)
-            v[i] = x[e - p.pairs] * sn[e - p.pairs] + v[i] * cs[e - p.pairs];
-        }
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(a[i] << 16);
+        v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
       }
     }
   }
-  if (live) {
-    if (is_q)
-      store8(p.qo, t * p.qo_rs + h * p.qo_hs + e0, p.out_f32, v);
-    else
-      store8(p.ko, t * p.ko_rs + h * p.ko_hs + e0, p.out_f32, v);
+};
+
+template <int G, int MODE, bool F32>
+__global__ void __launch_bounds__(kQkThreads, 3) qk_norm_rope_kernel(const QkParams p) {
+  __shared__ float xs[MODE == PAIR_SHARED ? kQkThreads * 16 : 1];
+  constexpr int ES = F32 ? 4 : 2;
+  const int lane = threadIdx.x & (G - 1);
+  const int chunks = (p.head_dim + 15) / 16;  // C
+  const int ea = lane * 8, eb = (chunks + lane) * 8;
+  const int heads = p.n_q + p.n_k;
+  const int64_t group = (int64_t)blockIdx.x * (kQkThreads / G) + threadIdx.x / G;
+  const int64_t block = group / heads;  // of `tokens` tokens
+  int h = (int)(group - block * heads);
+  const int64_t t0 = block * p.tokens;
+  const int n = t0 < p.T && lane < chunks ? (int)(p.T - t0 < p.tokens ? p.T - t0 : p.tokens) : 0;
+  const bool has_b = eb < p.head_dim;
+  const bool is_q = h < p.n_q;
+  if (!is_q) h -= p.n_q;
+  const int64_t rs = is_q ? p.q_rs : p.k_rs, ors = is_q ? p.qo_rs : p.ko_rs;
+  const int oes = p.out_f32 ? 4 : 2;
+  const char* src = static_cast<const char*>(is_q ? p.q : p.k) + ((is_q ? h * p.q_hs : h * p.k_hs) + t0 * rs + ea) * ES;
+  char* dst = static_cast<char*>(is_q ? p.qo : p.ko) + ((is_q ? h * p.qo_hs : h * p.ko_hs) + t0 * ors + ea) * oes;
+  const int64_t src_step = rs * ES, dst_step = ors * oes;
+  const int src_b = chunks * 8 * ES, dst_b = chunks * 8;  // second chunk: bytes, elements
+  const float* w = is_q ? p.w_q : p.w_k;
+  const bool norms = p.w_q != nullptr || p.w_k != nullptr;
+  const int step = p.pairs / 8;  // PAIR_SHUFFLE: lanes between partners
+  const bool lo = lane < step, hi = !lo && lane < 2 * step;
+  const int partner = lo ? lane + step : (hi ? lane - step : lane);
+  const int i0 = MODE == PAIR_OWN ? ea / 2 : MODE == PAIR_SHUFFLE && hi ? ea - p.pairs : ea;  // first pair of chunk a
+  const bool rotates = MODE == PAIR_OWN ? i0 < p.pairs : MODE == PAIR_LOCAL ? true : (lo || hi);
+  const bool rotates_b = MODE == PAIR_OWN && has_b && eb / 2 < p.pairs;
+  const bool vec = (p.pairs & 3) == 0;
+  const float* cs = p.cos + t0 * p.pairs;
+  const float* sn = p.sin + t0 * p.pairs;
+  griddep_wait();
+  griddep_trigger();
+  float wa[8] = {}, wb[8] = {};
+  if (w != nullptr && n > 0) {
+    load8_f32(w + ea, wa);
+    if (has_b) load8_f32(w + eb, wb);
   }
+
+  // (the same number of steps for every group: shuffles and __syncwarp need whole warps)
+  constexpr int TAB = MODE == PAIR_OWN ? 4 : MODE == PAIR_SHARED ? 1 : 8;
+  constexpr int TAB_B = MODE == PAIR_OWN ? 4 : 1;
+  RawChunk<F32> ra, rb;
+  float c[TAB], s[TAB], cb[TAB_B], sb[TAB_B];
+  auto request = [&](bool live) {  // the head and table rows that src, cs and sn point at
+    ra.load(src, live);
+    rb.load(src + src_b, live && has_b);
+    if constexpr (MODE != PAIR_SHARED) {
+      if (live && rotates) load_pairs<TAB>(cs, sn, i0, p.pairs, vec, c, s);
+      if constexpr (MODE == PAIR_OWN)
+        if (live && rotates_b) load_pairs<4>(cs, sn, eb / 2, p.pairs, vec, cb, sb);
+    }
+  };
+  for (int k = 0; k < p.tokens; ++k) {
+    const bool live = k < n;
+    request(live);
+    float a[8], b[8];
+    ra.unpack(a);
+    rb.unpack(b);
+    const float *cs_now = cs, *sn_now = sn;
+    src += src_step;
+    cs += p.pairs;
+    sn += p.pairs;
+    if (norms) {
+      float ss = 0.f, sq = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        ss = fmaf(a[i], a[i], ss);
+        sq = fmaf(b[i], b[i], sq);
+      }
+      ss += sq;
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (w != nullptr) {
+        const float r = rsqrtf(fmaf(ss, p.inv_dim, p.eps));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          a[i] = a[i] * r * wa[i];
+          b[i] = b[i] * r * wb[i];
+        }
+      }
+    }
+    if constexpr (MODE == PAIR_OWN) {
+      if (rotates) rotate_own(a, c, s, i0, p.pairs);
+      if (rotates_b) rotate_own(b, cb, sb, eb / 2, p.pairs);
+    } else if constexpr (MODE == PAIR_LOCAL) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = a[i], y = b[i];
+        a[i] = x * c[i] - y * s[i];
+        b[i] = x * s[i] + y * c[i];
+      }
+    } else if constexpr (MODE == PAIR_SHUFFLE) {
+      if (p.pairs > 0) {
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, a[i], partner, G);
+        if (rotates) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) a[i] = fmaf(a[i], c[i], lo ? -o[i] * s[i] : o[i] * s[i]);
+        }
+      }
+    } else {
+      float* x = xs + (threadIdx.x / G) * (G * 16);
+      __syncwarp();  // the previous token's readers are done
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[ea + i] = a[i];
+        if (eb + i < G * 16) x[eb + i] = b[i];
+      }
+      __syncwarp();
+      if (live) {
+        auto turn = [&](float v, int e) {
+          if (e < p.pairs) return v * cs_now[e] - x[e + p.pairs] * sn_now[e];
+          if (e < 2 * p.pairs) return x[e - p.pairs] * sn_now[e - p.pairs] + v * cs_now[e - p.pairs];
+          return v;
+        };
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          a[i] = turn(a[i], ea + i);
+          b[i] = turn(b[i], eb + i);
+        }
+      }
+    }
+    if (live) {
+      store8(dst, 0, p.out_f32, a);
+      if (has_b) store8(dst, dst_b, p.out_f32, b);
+    }
+    dst += dst_step;
+  }
+}
+
+template <int G, int MODE>
+cudaError_t launch_qk_mode(const QkParams& p, cudaStream_t s) {
+  const int64_t groups = (p.T + p.tokens - 1) / p.tokens * (p.n_q + p.n_k), per = kQkThreads / G;
+  const dim3 grid((unsigned)((groups + per - 1) / per));
+  return p.in_f32 ? launch_dependent(qk_norm_rope_kernel<G, MODE, true>, grid, dim3(kQkThreads), 0, s, p)
+                  : launch_dependent(qk_norm_rope_kernel<G, MODE, false>, grid, dim3(kQkThreads), 0, s, p);
 }
 
 template <int G>
 cudaError_t launch_qk_group(const QkParams& p, int mode, cudaStream_t s) {
-  const int64_t per = kQkThreads / G;
-  const dim3 grid((unsigned)((p.units + per - 1) / per));
   switch (mode) {
-    case PAIR_OWN: return launch_dependent(qk_norm_rope_kernel<G, PAIR_OWN>, grid, dim3(kQkThreads), 0, s, p);
-    case PAIR_SHUFFLE: return launch_dependent(qk_norm_rope_kernel<G, PAIR_SHUFFLE>, grid, dim3(kQkThreads), 0, s, p);
-    default: return launch_dependent(qk_norm_rope_kernel<G, PAIR_SHARED>, grid, dim3(kQkThreads), 0, s, p);
+    case PAIR_OWN: return launch_qk_mode<G, PAIR_OWN>(p, s);
+    case PAIR_LOCAL: return launch_qk_mode<G, PAIR_LOCAL>(p, s);
+    case PAIR_SHUFFLE: return launch_qk_mode<G, PAIR_SHUFFLE>(p, s);
+    default: return launch_qk_mode<G, PAIR_SHARED>(p, s);
   }
 }
 
@@ -299,7 +408,10 @@ ZDIT_API zdit_status zdit_rope_table_scaled(const int32_t* pos, int64_t T, int32
   if (T == 0) return ZDIT_OK;
   if (!device_ok()) return ZDIT_ERR_UNSUPPORTED;
   RopeScaledParams p;
-  p.pos = pos; p.T = T; p.pairs = rotary_dim / 2; p.theta = theta; p.factor = sc.factor;
+  p.pos = pos; p.T = T; p.pairs = rotary_dim / 2; p.factor = sc.factor;
+  p.log2_base = std::log2((double)theta);
+  if (sc.kind == ZDIT_ROPE_SCALE_NTK)
+    p.log2_base += (double)rotary_dim / (rotary_dim - 2.0) * std::log2((double)sc.factor);
   p.original_len = sc.original_len; p.beta_fast = sc.beta_fast; p.beta_slow = sc.beta_slow; p.kind = sc.kind;
   p.magnitude = sc.magnitude; p.cs = cos_out; p.sn = sin_out;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -340,22 +452,31 @@ ZDIT_API zdit_status zdit_qk_norm_rope(const zdit_qk_norm_rope_args* a, void* st
   if (a->T == 0) return ZDIT_OK;
   if (!device_ok()) return ZDIT_ERR_UNSUPPORTED;
   QkParams p;
-  p.units = a->T * heads; p.n_q = a->n_q; p.n_k = a->n_k; p.head_dim = a->head_dim; p.pairs = a->rotary_dim / 2;
+  p.T = a->T;
+  // tokens per group: 1 while that gives no more than about two waves of CTAs, up to 8
+  const int64_t lanes = a->T * heads * (a->head_dim <= 64 ? 4 : a->head_dim <= 128 ? 8 : 16);
+  const int64_t fill = lanes / ((int64_t)num_sms() * 2048 * 2);
+  p.tokens = (int)(fill < 1 ? 1 : fill > 8 ? 8 : fill);
+  p.n_q = a->n_q; p.n_k = a->n_k; p.head_dim = a->head_dim; p.pairs = a->rotary_dim / 2;
   p.q = a->q.ptr; p.k = a->k.ptr; p.qo = a->q_out.ptr; p.ko = a->k_out.ptr;
   p.q_rs = a->q.row_stride; p.q_hs = a->q.head_stride; p.k_rs = a->k.row_stride; p.k_hs = a->k.head_stride;
   p.qo_rs = a->q_out.row_stride; p.qo_hs = a->q_out.head_stride;
   p.ko_rs = a->k_out.row_stride; p.ko_hs = a->k_out.head_stride;
   p.w_q = a->w_q; p.w_k = a->w_k; p.cos = a->cos; p.sin = a->sin; p.eps = a->eps; p.inv_dim = 1.0f / a->head_dim;
   p.in_f32 = a->in_dtype == ZDIT_T_F32; p.out_f32 = a->out_dtype == ZDIT_T_F32;
-  const int mode = a->layout == ZDIT_ROPE_INTERLEAVED ? PAIR_OWN : (p.pairs % 8 == 0 ? PAIR_SHUFFLE : PAIR_SHARED);
+  const int half = (a->head_dim + 15) / 16 * 8;  // first element of the second chunks
+  const int mode = a->layout == ZDIT_ROPE_INTERLEAVED          ? PAIR_OWN
+                   : p.pairs == half && a->rotary_dim == a->head_dim ? PAIR_LOCAL
+                   : p.pairs % 8 == 0 && a->rotary_dim <= half ? PAIR_SHUFFLE
+                                                               : PAIR_SHARED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const double elems = (double)p.units * p.head_dim;
+  const double elems = (double)a->T * heads * p.head_dim;
   ProfScope ps(PROF_NORM_MOD, 7.0 * elems,
                elems * ((p.in_f32 ? 4 : 2) + (p.out_f32 ? 4 : 2)) + 8.0 * a->T * p.pairs, s);
   cudaError_t e;
-  if (a->head_dim <= 64) e = launch_qk_group<8>(p, mode, s);
-  else if (a->head_dim <= 128) e = launch_qk_group<16>(p, mode, s);
-  else e = launch_qk_group<32>(p, mode, s);
+  if (a->head_dim <= 64) e = launch_qk_group<4>(p, mode, s);
+  else if (a->head_dim <= 128) e = launch_qk_group<8>(p, mode, s);
+  else e = launch_qk_group<16>(p, mode, s);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ZDIT_OK : ZDIT_ERR_CUDA;
 }
 
