@@ -8,32 +8,32 @@
 // are read once per key head, a single token fills `group` rows instead of one, and the mask
 // is a limit on the key index that depends on the row's token alone.
 //
-// Two kernels share that layout:
+// One CTA takes one query tile (sequence, 128 rows, key head, part of the keys), two CTAs per
+// SM, so that one CTA's set-up, loads and output overlap the other's work; 64-key tiles with S
+// double-buffered in TMEM, so that S of the next tile is ready when the softmax finishes the
+// last one.  7 warps: 0-3 softmax, one thread per row; 4 loads Q and K; 5 issues the MMAs; 6
+// loads V (its own warp: a V stage still in use never delays the next K).
+// TMEM columns: S buffers [0, 64) and [64, 128), O [128, +HD).  P (bf16 pairs) is written over
+// the first columns of its S and feeds the PV product from there.  Softmax in fp32: a running
+// maximum that moves only when a row grows by more than 16 (log2 units; P <= 2^16 keeps bf16's
+// relative precision), and the sum of the unrounded P.
+// Per 128 x 64 unit the tensor core works 8 x 48 + 4 x 64 = 640 clocks (S reads both operands
+// from shared memory, 48 clocks a step instead of 32), the exponentials take 512, and shared
+// memory moves 32 KB of K and V in and 64 KB of operands out, 768: long prompts are bound
+// there (16384 tokens, 32 heads on 8: 1.85 ms, 1190 TFLOP/s); a short item is mostly set-up,
+// load latency and output (one key tile 4.8 us, 0.65 us for each further one).
+// Measured and not kept: two query tiles and 128-key tiles per CTA, one CTA per SM (half the K
+// and V traffic, but it waits for its own softmax: 1.0 to 1.6 times slower from 300 to 16384
+// tokens with 8 key heads); a persistent kernel that loads the next item while it finishes the
+// last (its bookkeeping costs 1 us an item and the static shares are uneven: 1.2 to 1.4 times
+// slower).
 //
-// prompt_attn_wide: long prompts (arithmetic-bound).  One CTA per SM takes two query tiles
-//   and all their key tiles (128 keys), so that each K and V tile in shared memory feeds 256
-//   rows.  384 threads: warps 0-3 and 4-7 are the softmax of slots 0 and 1, one thread per
-//   row; warp 8 loads Q and K, warp 9 issues the MMAs, warp 10 loads V (its own warp, so that
-//   a V stage still in use never delays the next K), warp 11 completes the warpgroup that
-//   hands registers over (168 per thread at launch -> 208 softmax, 88 control: 2 x 128 x 208
-//   + 128 x 88 = 64512).  The last tile of an odd number has its even and odd key tiles on
-//   the two slots, joined in shared memory.
-// prompt_attn_narrow: short prompts, new rows after a prefix, single tokens (latency- and
-//   memory-bound).  One query tile per CTA, two CTAs per SM, so that one CTA's set-up, loads
-//   and output overlap the other's work; 64-key tiles with S double-buffered in TMEM, so that
-//   S of the next tile is ready when the softmax finishes the last one.  Keys are split over
-//   CTAs when the rows do not fill the GPU: each part writes its normalised O (fp32) with its
-//   maximum and sum to the workspace, and a third kernel joins the parts of a row in
-//   ascending order.
-//
-// In both, P (bf16 pairs) is written over the first columns of its S in TMEM and feeds the
-// PV product from there.  Softmax in fp32: a running maximum that moves only when a row grows
-// by more than 16 (log2 units; P <= 2^16 keeps bf16's relative precision), and the sum of the
-// unrounded P.
+// Keys are split over CTAs when the items do not fill the GPU: each part writes its normalised
+// O (fp32) with its maximum and sum to the workspace, and a second kernel joins the parts of a
+// row in a fixed order.
 #include <algorithm>
 #include <climits>
 #include <cmath>
-#include <cstdlib>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -46,12 +46,10 @@ bool heads_disjoint(const zdit_heads& h, int64_t rows, int heads, int head_dim);
 
 namespace {
 
-constexpr int TILE = 128;       // rows of a query tile, keys of a key tile of the wide kernel
-constexpr int NTILE = 64;       // keys of a key tile of the narrow kernel
-constexpr int THREADS = 384;    // wide
-constexpr int WARP_QK = 8, WARP_MMA = 9, WARP_V = 10;
-constexpr int NTHREADS = 224;   // narrow: 4 softmax warps, Q and K, MMA, V
-constexpr int NWARP_QK = 4, NWARP_MMA = 5, NWARP_V = 6;
+constexpr int TILE = 128;       // rows of a query tile
+constexpr int KTILE = 64;       // keys of a key tile
+constexpr int THREADS = 224;
+constexpr int WARP_QK = 4, WARP_MMA = 5, WARP_V = 6;
 constexpr int kMaxSeqs = 128;
 constexpr float kRescaleThreshold = 16.0f;  // log2 units
 
@@ -60,14 +58,15 @@ struct Plan {
   int n;  // sequences with query rows
   int item0[kMaxSeqs + 1];  // first item (per key head) of sequence i; item0[n] = all
   int q0[kMaxSeqs], q_len[kMaxSeqs], kv0[kMaxSeqs], kv_len[kMaxSeqs];
-  int parts[kMaxSeqs];      // key splits (narrow kernel)
-  int chunk[kMaxSeqs];      // keys of a part, a multiple of NTILE
+  int parts[kMaxSeqs];      // key splits
+  int chunk[kMaxSeqs];      // keys of a part, a multiple of KTILE
   int part0[kMaxSeqs];      // first partial row of the sequence in the workspace (parts > 1)
   int join0[kMaxSeqs + 1];  // first joined row (token, head) among sequences with parts > 1
 };
 
 struct PParams {
   int n_kv, group, tokens;  // tokens per query tile
+  int heads_at_once;        // key heads whose items are interleaved
   int causal;
   float scale_log2;
   __nv_bfloat16* o;
@@ -79,15 +78,15 @@ struct PParams {
 
 template <int HD>
 struct Cfg {
-  static constexpr int HALF = TILE * 128;               // 64 columns x 128 rows, 16 KB
+  static constexpr int Q_HALF = TILE * 128;              // 64 columns x 128 rows
+  static constexpr int Q_BYTES = (HD / 64) * Q_HALF;
+  static constexpr int HALF = KTILE * 128;               // 64 columns x 64 keys, 8 KB
   static constexpr int TILE_BYTES = (HD / 64) * HALF;
-  static constexpr int ST = HD == 128 ? 2 : 4;          // K and V ring depth (64 KB each)
-  static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = 2 * TILE_BYTES;
+  static constexpr int ST = HD == 128 ? 2 : 4;           // ring depth of K and of V (32 KB each)
+  static constexpr int OFF_K = Q_BYTES;
   static constexpr int OFF_V = OFF_K + ST * TILE_BYTES;
   static constexpr int OFF_BAR = OFF_V + ST * TILE_BYTES;
-  static constexpr int SMEM = 1024 + OFF_BAR + 256;
-  static constexpr int JOIN_ROW = HD + 4;               // fp32 row of slot 1 when slots are joined
+  static constexpr int SMEM = 1024 + OFF_BAR + 256;      // two CTAs fit an SM
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -124,20 +123,16 @@ __device__ __forceinline__ int last_key(int tok, int q_len, int kv_len, int caus
   return causal ? min(tok + kv_len - q_len, kv_len - 1) : kv_len - 1;
 }
 
-// Item `item` (per key head): its sequence and its index inside the sequence.
-__device__ __forceinline__ int find_item(const Plan& plan, int item, int& rem) {
+// Index of the sequence that item `item` (per key head) belongs to.
+__device__ __forceinline__ int find_item(const Plan& plan, int item) {
   int lo = 0, hi = plan.n;  // plan.item0[lo] <= item < plan.item0[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (plan.item0[mid] <= item) lo = mid; else hi = mid;
   }
-  rem = item - plan.item0[lo];
   return lo;
 }
 
-// Running softmax of one row over a tile of N logits in s: moves the reference maximum if
-// needed (alpha then scales what was accumulated so far), replaces s by P = exp2(s scale -
-// m_ref) packed as bf16 pairs in pk and returns the sum of the unrounded P.
 template <int N>
 __device__ __forceinline__ float row_max(const float (&s)[N]) {
   float m8[8];  // independent chains of 3-input max
@@ -150,6 +145,8 @@ __device__ __forceinline__ float row_max(const float (&s)[N]) {
   return fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], fmax3(m8[5], m8[6], m8[7])));
 }
 
+// P = exp2(s scale - m_use) of one row over a tile of N logits, stored as bf16 pairs over the
+// tile's first columns of TMEM; returns the sum of the unrounded P.
 template <int N>
 __device__ __forceinline__ float row_exp(const float (&s)[N], float scale_log2, float m_use, uint32_t tS) {
   const uint64_t sc2 = pk2(scale_log2, scale_log2);
@@ -228,352 +225,11 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, int lane, long long o
 }
 
 template <int HD>
-__global__ void __launch_bounds__(THREADS, 1)
-    prompt_attn_wide_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Plan plan, const PParams p) {
-  using C = Cfg<HD>;
-  constexpr int ST = C::ST;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* q_full = bars;              // [2]
-  uint64_t* s_full = bars + 2;          // [2]
-  uint64_t* p_full = bars + 4;          // [2]
-  uint64_t* o_full = bars + 6;          // [2]
-  uint64_t* mma_done = bars + 8;
-  uint64_t* k_full = bars + 9;          // [ST]
-  uint64_t* k_empty = k_full + ST;      // [ST]
-  uint64_t* v_full = k_empty + ST;      // [ST]
-  uint64_t* v_empty = v_full + ST;      // [ST]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_empty + ST);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-
-  const int warp = threadIdx.x >> 5;
-  const int lane = threadIdx.x & 31;
-  griddep_wait();     // Q, K, V of the predecessor are complete, the workspace is free
-  griddep_trigger();  // every CTA has started: the successor may launch
-
-  // item of this CTA: key heads fastest, so that all heavy items come first
-  const int item = blockIdx.x / p.n_kv;
-  const int kvh = blockIdx.x - item * p.n_kv;
-  int rem;
-  const int sq = find_item(plan, item, rem);
-  const int q_len = plan.q_len[sq], kv_len = plan.kv_len[sq], kv0 = plan.kv0[sq], q0 = plan.q0[sq];
-  const int n_pairs = (q_len + 2 * p.tokens - 1) / (2 * p.tokens);
-  const int tok0 = (n_pairs - 1 - rem) * 2 * p.tokens;  // later rows see more keys: first
-  const bool two = tok0 + p.tokens < q_len;             // two query tiles, or one with split keys
-  // key tiles [0, n) of this item; slot 0 of two stops after n0
-  auto tiles_for = [&](int tok_end) {
-    const int lk = last_key(min(tok_end, q_len) - 1, q_len, kv_len, p.causal);
-    return lk < 0 ? 0 : lk / TILE + 1;
-  };
-  const int n0 = tiles_for(tok0 + p.tokens);
-  const int n = two ? tiles_for(tok0 + 2 * p.tokens) : n0;
-
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
-      mbar_init(&o_full[i], 1);
-    }
-    for (int i = 0; i < ST; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
-    }
-    mbar_init(mma_done, 1);
-    *abort_flag = 0;
-    fence_barrier_init();
-  }
-  if (warp == WARP_QK && lane == 0) {
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-  }
-  if (warp == WARP_V && lane == 0) tma_prefetch_desc(&tmV);
-  if (warp == WARP_MMA) tmem_alloc(tmem_slot, 512);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::: "memory");
-    if (warp == WARP_QK && lane == 0 && n > 0) {
-      // ------------------------------------------------------------ Q and K
-      const uint32_t q_bytes = (uint32_t)(p.group * p.tokens * 128 * (HD / 64));
-      auto load_q = [&](int t) {
-        uint8_t* sQ = smem + C::OFF_Q + t * C::TILE_BYTES;
-        mbar_arrive_expect_tx(&q_full[t], q_bytes);
-        for (int c = 0; c < HD / 64; ++c)
-          tma_load_3d(sQ + c * C::HALF, &tmQ, &q_full[t], c * 64, kvh * p.group, q0 + tok0 + t * p.tokens);
-      };
-      load_q(0);
-      int issued = 0;
-      for (int i = 0; i < n; ++i) {
-        const int st = i % ST;
-        if (!mbar_wait(&k_empty[st], ((i / ST) & 1) ^ 1, abort_flag, p.err)) break;
-        uint8_t* sK = smem + C::OFF_K + st * C::TILE_BYTES;
-        mbar_arrive_expect_tx(&k_full[st], C::TILE_BYTES);
-        for (int c = 0; c < HD / 64; ++c)
-          tma_load_3d(sK + c * C::HALF, &tmK, &k_full[st], c * 64, kvh, kv0 + i * TILE);
-        ++issued;
-        if (i == 0 && two) load_q(1);
-      }
-      if (*abort_flag) {  // let copies in flight land before shared memory is released
-        int dummy = 0;
-        mbar_wait(&q_full[0], 0, &dummy);
-        if (two && issued > 0) mbar_wait(&q_full[1], 0, &dummy);
-        for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(&k_full[i % ST], (i / ST) & 1, &dummy);
-      }
-    } else if (warp == WARP_V && lane == 0) {
-      // ------------------------------------------------------------ V
-      int issued = 0;
-      for (int i = 0; i < n; ++i) {
-        const int st = i % ST;
-        if (!mbar_wait(&v_empty[st], ((i / ST) & 1) ^ 1, abort_flag, p.err)) break;
-        uint8_t* sV = smem + C::OFF_V + st * C::TILE_BYTES;
-        mbar_arrive_expect_tx(&v_full[st], C::TILE_BYTES);
-        for (int c = 0; c < HD / 64; ++c)
-          tma_load_3d(sV + c * C::HALF, &tmV, &v_full[st], c * 64, kvh, kv0 + i * TILE);
-        ++issued;
-      }
-      if (*abort_flag) {
-        int dummy = 0;
-        for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(&v_full[i % ST], (i / ST) & 1, &dummy);
-      }
-    } else if (warp == WARP_MMA && lane == 0 && n > 0) {
-      // ------------------------------------------------------------ MMA issuer
-      const uint32_t id_s = idesc_bf16_f32(TILE, TILE);             // Q, K both K-major
-      const uint32_t id_o = idesc_bf16_f32(TILE, HD, false, true);  // P from TMEM, V MN-major
-      const uint64_t dq = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_Q));
-      const uint64_t dk = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_K));
-      const uint64_t dv = sdesc_mnmajor_sw128(smem_u32(smem + C::OFF_V), C::HALF, 1024);
-      constexpr uint64_t kTileDesc = C::TILE_BYTES >> 4;  // descriptors are linear in the address
-      auto koff = [](int k) -> uint64_t { return (uint64_t)(((k >> 2) * C::HALF + (k & 3) * 32) >> 4); };
-      auto voff = [](int k) -> uint64_t { return (uint64_t)((k * 16 * 128) >> 4); };
-      // O_t (+)= P_t V_i, the c-th product of slot t
-      auto pv = [&](int t, int i, int c) -> bool {
-        if (!mbar_wait(&p_full[t], c & 1, abort_flag, p.err)) return false;
-        if (!mbar_wait(&v_full[i % ST], (i / ST) & 1, abort_flag, p.err)) return false;
-        tc_fence_after();
-        const uint64_t vb = dv + (i % ST) * kTileDesc;
-        const uint32_t d = tmem + 256 + t * 128, pa = tmem + t * 128;
-        umma_bf16_ts(d, pa, vb, id_o, c != 0 ? 1u : 0u);
-#pragma unroll
-        for (int k = 1; k < TILE / 16; ++k) umma_bf16_ts(d, pa + k * 8, vb + voff(k), id_o, 1u);
-        return true;
-      };
-      // S_t = Q_qt K_i^T
-      auto sk = [&](int t, int qt, int i) {
-        const uint64_t kb = dk + (i % ST) * kTileDesc, qb = dq + qt * kTileDesc;
-        const uint32_t d = tmem + t * 128;
-        umma_bf16_ss(d, qb, kb, id_s, 0u);
-#pragma unroll
-        for (int k = 1; k < HD / 16; ++k) umma_bf16_ss(d, qb + koff(k), kb + koff(k), id_s, 1u);
-        umma_commit(&s_full[t]);
-      };
-      bool ok = mbar_wait(&q_full[0], 0, abort_flag, p.err);
-      if (two) {
-        for (int i = 0; ok && i < n; ++i) {
-          if (!(ok = mbar_wait(&k_full[i % ST], (i / ST) & 1, abort_flag, p.err))) break;
-          tc_fence_after();
-          if (i > 0 && i <= n0 && !(ok = pv(0, i - 1, i - 1))) break;
-          if (i < n0) sk(0, 0, i);
-          if (i > 0) {
-            if (!(ok = pv(1, i - 1, i - 1))) break;
-            umma_commit(&v_empty[(i - 1) % ST]);
-          }
-          if (i == 0 && !(ok = mbar_wait(&q_full[1], 0, abort_flag, p.err))) break;
-          sk(1, 1, i);
-          umma_commit(&k_empty[i % ST]);
-        }
-        if (ok && n0 == n) ok = pv(0, n - 1, n - 1);
-        if (ok) umma_commit(&o_full[0]);  // after every S product: Q and K are idle
-        if (ok && pv(1, n - 1, n - 1)) umma_commit(&o_full[1]);
-      } else {
-        for (int i = 0; ok && i < n; ++i) {
-          if (!(ok = mbar_wait(&k_full[i % ST], (i / ST) & 1, abort_flag, p.err))) break;
-          tc_fence_after();
-          const int t = i & 1;
-          if (i > 1) {
-            if (!(ok = pv(t, i - 2, (i >> 1) - 1))) break;
-            umma_commit(&v_empty[(i - 2) % ST]);
-          }
-          sk(t, 0, i);
-          umma_commit(&k_empty[i % ST]);
-        }
-        if (ok && n > 1 && (ok = pv(n & 1, n - 2, (n - 2) >> 1))) umma_commit(&o_full[n & 1]);
-        if (ok && pv((n - 1) & 1, n - 1, (n - 1) >> 1)) umma_commit(&o_full[(n - 1) & 1]);
-      }
-      umma_commit(mma_done);
-      int dummy = 0;
-      mbar_wait(mma_done, 0, &dummy);
-    }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n" ::: "memory");
-    // ------------------------------------------------------------ softmax
-    const int t = warp >> 2;   // slot
-    const int lg = warp & 3;   // TMEM lane group
-    const int row = lg * 32 + lane;
-    const int tok = tok0 + (two ? t * p.tokens : 0) + row / p.group;
-    const int head = kvh * p.group + row % p.group;
-    const bool live = row < p.group * p.tokens && tok < q_len;
-    const bool warp_live = __any_sync(0xffffffffu, live);
-    const int lim = live ? last_key(tok, q_len, kv_len, p.causal) : kv_len - 1;
-    const uint32_t lane_off = (uint32_t)(lg * 32) << 16;
-    const uint32_t tS = tmem + lane_off + t * 128;
-    const uint32_t tO = tmem + lane_off + 256 + t * 128;
-    const int cnt = two ? (t == 0 ? n0 : n) : (n + 1 - t) >> 1;
-    float m_ref = -INFINITY, l_sum = 0.f;
-    bool ok = true;
-    for (int c = 0; c < cnt; ++c) {
-      const int i = two ? c : 2 * c + t;
-      const int key0 = i * TILE;
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], c & 1, abort_flag, p.err));
-      if (!ok) break;
-      tc_fence_after();
-      if (key0 + TILE > kv_len && (!two || t == 0 || i >= n0)) {
-        // (by the slot that uses the tile first)
-        ok = __all_sync(0xffffffffu, mbar_wait(&v_full[i % ST], (i / ST) & 1, abort_flag, p.err));
-        if (!ok) break;
-        if (row >= kv_len - key0) clear_v_row<HD>(smem + C::OFF_V + (i % ST) * C::TILE_BYTES, C::HALF, row);
-        fence_proxy_async_smem();
-      }
-      if (warp_live) {
-        float s[TILE];
-#pragma unroll
-        for (int e4 = 0; e4 < 4; ++e4) {
-          uint32_t r[32];
-          tmem_ld32(tS + e4 * 32, r);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) s[e4 * 32 + e] = __uint_as_float(r[e]);
-        }
-        tmem_ld_wait();
-        const int valid = lim - key0;  // last allowed column of this tile
-        if (valid < TILE - 1) {
-#pragma unroll
-          for (int e = 0; e < TILE; ++e)
-            if (e > valid) s[e] = -INFINITY;
-        }
-        const float mx = row_max<TILE>(s) * p.scale_log2;
-        float alpha = 1.f;
-        bool move = false;
-        if (c == 0) {
-          m_ref = mx;
-        } else if (mx > m_ref + kRescaleThreshold) {
-          alpha = ex2(m_ref - mx);
-          m_ref = mx;
-          move = true;
-        }
-        // O is stable: the previous PV completed before this S
-        if (__any_sync(0xffffffffu, move)) scale_o<HD>(tO, alpha);
-        // (a row with no key yet has m_ref = -inf: with 0 in its place P is 0)
-        l_sum = l_sum * alpha + row_exp<TILE>(s, p.scale_log2, m_ref == -INFINITY ? 0.f : m_ref, tS);
-        tmem_st_wait();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[t]);
-    }
-    // ------------------------------------------------------------ epilogue
-    // Both slots' products are awaited before shared memory is reused for staging.
-    if (ok && (cnt > 0 || (two && n > 0)))
-      ok = __all_sync(0xffffffffu, mbar_wait(&o_full[t], 0, abort_flag, p.err));
-    tc_fence_after();
-    float wa = 1.f, wb = 0.f;  // weights of this slot's O and of slot 1's when joined
-    float* join = reinterpret_cast<float*>(smem + C::OFF_V / 2);
-    float2* join_ml = reinterpret_cast<float2*>(smem + C::OFF_V / 2 + TILE * C::JOIN_ROW * 4);
-    if (!two && n > 1) {
-      if (t == 1) {
-        // slot 0's last S product may still read K here: wait for everything
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&o_full[0], 0, abort_flag, p.err));
-        if (ok && warp_live) {
-          for (int e4 = 0; e4 < HD / 32; ++e4) {
-            uint32_t r[32];
-            tmem_ld32(tO + e4 * 32, r);
-            tmem_ld_wait();
-            float4* dst = reinterpret_cast<float4*>(join + row * C::JOIN_ROW + e4 * 32);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              dst[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]),
-                                   __uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3]));
-          }
-          join_ml[row] = make_float2(m_ref, l_sum);
-        }
-      }
-      named_bar_sync(1, 256);
-      if (t == 0) {
-        const float2 b = join_ml[row];
-        const float m = fmaxf(m_ref, b.x), mu = m == -INFINITY ? 0.f : m;
-        wa = ex2(m_ref - mu);
-        wb = ex2(b.x - mu);
-        l_sum = l_sum * wa + b.y * wb;
-        m_ref = m;
-      }
-    }
-    if (ok && (two || t == 0)) {
-      const float inv = l_sum == 0.f ? 0.f : 1.0f / l_sum;
-      wa *= inv;
-      wb *= inv;
-      const bool joined = !two && n > 1;
-      auto take = [&](int e4, float (&v)[32]) {  // 32 columns of the finished row
-        if (cnt > 0) {
-          uint32_t r[32];
-          tmem_ld32(tO + e4 * 32, r);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]) * wa;
-          if (joined) {
-            const float4* src = reinterpret_cast<const float4*>(join + row * C::JOIN_ROW + e4 * 32);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 q = src[e];
-              v[4 * e] = fmaf(q.x, wb, v[4 * e]);
-              v[4 * e + 1] = fmaf(q.y, wb, v[4 * e + 1]);
-              v[4 * e + 2] = fmaf(q.z, wb, v[4 * e + 2]);
-              v[4 * e + 3] = fmaf(q.w, wb, v[4 * e + 3]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0.f;
-        }
-      };
-      if (warp_live)  // staged in the idle Q and K space of this slot
-        store_rows<HD>(smem + C::OFF_Q + t * (C::OFF_V / 2) + lg * 32 * (2 * HD + 16), lane,
-                       live ? (q0 + (int64_t)tok) * p.o_rs + head * p.o_hs : -1, p.o, take);
-    }
-    tc_fence_before();
-  }
-  __syncthreads();
-  if (warp == WARP_MMA) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 512);
-  }
-}
-
-template <int HD>
-struct NCfg {
-  static constexpr int Q_HALF = TILE * 128;              // 64 columns x 128 rows
-  static constexpr int Q_BYTES = (HD / 64) * Q_HALF;
-  static constexpr int HALF = NTILE * 128;               // 64 columns x 64 keys, 8 KB
-  static constexpr int TILE_BYTES = (HD / 64) * HALF;
-  static constexpr int ST = HD == 128 ? 2 : 4;           // ring depth of K and of V (32 KB each)
-  static constexpr int OFF_K = Q_BYTES;
-  static constexpr int OFF_V = OFF_K + ST * TILE_BYTES;
-  static constexpr int OFF_BAR = OFF_V + ST * TILE_BYTES;
-  static constexpr int SMEM = 1024 + OFF_BAR + 256;      // two CTAs fit an SM
-};
-
-// TMEM columns: S buffers [0,64) and [64,128), O [128, +HD); 256 per CTA.
-template <int HD>
-__global__ void __launch_bounds__(NTHREADS, 2)
-    prompt_attn_narrow_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+__global__ void __launch_bounds__(THREADS, 2)
+    prompt_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Plan plan,
                               const PParams p) {
-  using C = NCfg<HD>;
+  using C = Cfg<HD>;
   constexpr int ST = C::ST;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -609,21 +265,26 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == NWARP_QK && lane == 0) {
+  if (warp == WARP_QK && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
   }
-  if (warp == NWARP_V && lane == 0) tma_prefetch_desc(&tmV);
-  if (warp == NWARP_MMA) tmem_alloc(tmem_slot, 256);
+  if (warp == WARP_V && lane == 0) tma_prefetch_desc(&tmV);
+  if (warp == WARP_MMA) tmem_alloc(tmem_slot, 256);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int item = blockIdx.x / p.n_kv;
-  const int kvh = blockIdx.x - item * p.n_kv;
-  int rem;
-  const int sq = find_item(plan, item, rem);
+  // Items are ordered by groups of heads_at_once key heads (whose keys fit the L2 cache
+  // together), in a group by decreasing work, the heads of one item next to each other.
+  const int per_group = plan.item0[plan.n] * p.heads_at_once;
+  const int hg = blockIdx.x / per_group, in_group = blockIdx.x - hg * per_group;
+  const int heads = min(p.heads_at_once, p.n_kv - hg * p.heads_at_once);
+  const int item = in_group / heads;
+  const int kvh = hg * p.heads_at_once + in_group - item * heads;
+  const int sq = find_item(plan, item);
+  const int rem = item - plan.item0[sq];
   const int q_len = plan.q_len[sq], kv_len = plan.kv_len[sq], kv0 = plan.kv0[sq], q0 = plan.q0[sq];
   const int parts = plan.parts[sq], chunk = plan.chunk[sq];
   const int n_tiles = (q_len + p.tokens - 1) / p.tokens;
@@ -634,12 +295,12 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   {
     const int lk = last_key(min(tok0 + p.tokens, q_len) - 1, q_len, kv_len, p.causal);
     const int end = parts > 1 ? min(lk + 1, key_first + chunk) : lk + 1;
-    n = end > key_first ? (end - key_first + NTILE - 1) / NTILE : 0;
+    n = end > key_first ? (end - key_first + KTILE - 1) / KTILE : 0;
   }
   griddep_wait();     // Q, K, V of the predecessor are complete, the workspace is free
   griddep_trigger();  // every CTA has started: the successor may launch
 
-  if (warp == NWARP_QK) {
+  if (warp == WARP_QK) {
     if (lane == 0 && n > 0) {
       // ------------------------------------------------------------ Q and K
       mbar_arrive_expect_tx(q_full, (uint32_t)(p.group * p.tokens * 128 * (HD / 64)));
@@ -652,7 +313,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         uint8_t* sK = smem + C::OFF_K + st * C::TILE_BYTES;
         mbar_arrive_expect_tx(&k_full[st], C::TILE_BYTES);
         for (int c = 0; c < HD / 64; ++c)
-          tma_load_3d(sK + c * C::HALF, &tmK, &k_full[st], c * 64, kvh, kv0 + key_first + i * NTILE);
+          tma_load_3d(sK + c * C::HALF, &tmK, &k_full[st], c * 64, kvh, kv0 + key_first + i * KTILE);
         ++issued;
       }
       if (*abort_flag) {  // let copies in flight land before shared memory is released
@@ -661,7 +322,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(&k_full[i % ST], (i / ST) & 1, &dummy);
       }
     }
-  } else if (warp == NWARP_V) {
+  } else if (warp == WARP_V) {
     if (lane == 0) {
       // ------------------------------------------------------------ V
       int issued = 0;
@@ -671,7 +332,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         uint8_t* sV = smem + C::OFF_V + st * C::TILE_BYTES;
         mbar_arrive_expect_tx(&v_full[st], C::TILE_BYTES);
         for (int c = 0; c < HD / 64; ++c)
-          tma_load_3d(sV + c * C::HALF, &tmV, &v_full[st], c * 64, kvh, kv0 + key_first + i * NTILE);
+          tma_load_3d(sV + c * C::HALF, &tmV, &v_full[st], c * 64, kvh, kv0 + key_first + i * KTILE);
         ++issued;
       }
       if (*abort_flag) {
@@ -679,10 +340,10 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(&v_full[i % ST], (i / ST) & 1, &dummy);
       }
     }
-  } else if (warp == NWARP_MMA) {
+  } else if (warp == WARP_MMA) {
     if (lane == 0 && n > 0) {
       // ------------------------------------------------------------ MMA issuer
-      const uint32_t id_s = idesc_bf16_f32(TILE, NTILE);            // Q, K both K-major
+      const uint32_t id_s = idesc_bf16_f32(TILE, KTILE);            // Q, K both K-major
       const uint32_t id_o = idesc_bf16_f32(TILE, HD, false, true);  // P from TMEM, V MN-major
       const uint64_t dq = sdesc_kmajor_sw128(smem_u32(smem));
       const uint64_t dk = sdesc_kmajor_sw128(smem_u32(smem + C::OFF_K));
@@ -694,7 +355,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         if (!mbar_wait(&k_full[i % ST], (i / ST) & 1, abort_flag, p.err)) return false;
         tc_fence_after();
         const uint64_t kb = dk + (i % ST) * kTileDesc;
-        const uint32_t d = tmem + (i & 1) * NTILE;
+        const uint32_t d = tmem + (i & 1) * KTILE;
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k)
           umma_bf16_ss(d, dq + (uint64_t)(((k >> 2) * C::Q_HALF + (k & 3) * 32) >> 4),
@@ -710,10 +371,10 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         if (!(ok = mbar_wait(&v_full[i % ST], (i / ST) & 1, abort_flag, p.err))) break;
         tc_fence_after();
         const uint64_t vb = dv + (i % ST) * kTileDesc;
-        const uint32_t pa = tmem + (i & 1) * NTILE;
+        const uint32_t pa = tmem + (i & 1) * KTILE;
 #pragma unroll
-        for (int k = 0; k < NTILE / 16; ++k)
-          umma_bf16_ts(tmem + 2 * NTILE, pa + k * 8, vb + (uint64_t)((k * 16 * 128) >> 4), id_o, (i | k) != 0 ? 1u : 0u);
+        for (int k = 0; k < KTILE / 16; ++k)
+          umma_bf16_ts(tmem + 2 * KTILE, pa + k * 8, vb + (uint64_t)((k * 16 * 128) >> 4), id_o, (i | k) != 0 ? 1u : 0u);
         umma_commit(pv_done);
         umma_commit(&v_empty[i % ST]);
         if (i + 2 < n) ok = sk(i + 2);
@@ -731,26 +392,26 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     const bool warp_live = __any_sync(0xffffffffu, live);
     const int lim = live ? last_key(tok, q_len, kv_len, p.causal) : kv_len - 1;
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-    const uint32_t tO = tmem + lane_off + 2 * NTILE;
+    const uint32_t tO = tmem + lane_off + 2 * KTILE;
     float m_ref = -INFINITY, l_sum = 0.f;
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      const int key0 = key_first + i * NTILE;
+      const int key0 = key_first + i * KTILE;
       ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i & 1], (i >> 1) & 1, abort_flag, p.err));
       if (!ok) break;
       tc_fence_after();
-      if (key0 + NTILE > kv_len) {
+      if (key0 + KTILE > kv_len) {
         ok = __all_sync(0xffffffffu, mbar_wait(&v_full[i % ST], (i / ST) & 1, abort_flag, p.err));
         if (!ok) break;
-        if (row < NTILE && row >= kv_len - key0)
+        if (row < KTILE && row >= kv_len - key0)
           clear_v_row<HD>(smem + C::OFF_V + (i % ST) * C::TILE_BYTES, C::HALF, row);
         fence_proxy_async_smem();
       }
       if (warp_live) {
-        const uint32_t tS = tmem + lane_off + (i & 1) * NTILE;
-        float s[NTILE];
+        const uint32_t tS = tmem + lane_off + (i & 1) * KTILE;
+        float s[KTILE];
 #pragma unroll
-        for (int e4 = 0; e4 < NTILE / 32; ++e4) {
+        for (int e4 = 0; e4 < KTILE / 32; ++e4) {
           uint32_t r[32];
           tmem_ld32(tS + e4 * 32, r);
 #pragma unroll
@@ -758,12 +419,12 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         }
         tmem_ld_wait();
         const int valid = lim - key0;  // last allowed column of this tile
-        if (valid < NTILE - 1) {
+        if (valid < KTILE - 1) {
 #pragma unroll
-          for (int e = 0; e < NTILE; ++e)
+          for (int e = 0; e < KTILE; ++e)
             if (e > valid) s[e] = -INFINITY;
         }
-        const float mx = row_max<NTILE>(s) * p.scale_log2;
+        const float mx = row_max<KTILE>(s) * p.scale_log2;
         float alpha = 1.f;
         bool move = false;
         if (i == 0) {
@@ -781,7 +442,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           tc_fence_after();
           scale_o<HD>(tO, alpha);
         }
-        l_sum = l_sum * alpha + row_exp<NTILE>(s, p.scale_log2, m_ref == -INFINITY ? 0.f : m_ref, tS);
+        l_sum = l_sum * alpha + row_exp<KTILE>(s, p.scale_log2, m_ref == -INFINITY ? 0.f : m_ref, tS);
         tmem_st_wait();
       }
       tc_fence_before();
@@ -828,25 +489,29 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == NWARP_MMA) {
+  if (warp == WARP_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
 }
 
 // Joins the parts of a split row: O = sum_s w_s O_s / sum_s w_s, w_s = l_s 2^(m_s - max m).
-// One CTA per (token, head) row; warp w takes the parts w, w + 4, ..., the warps' sums are
-// added in order (the result does not depend on timing).  A chain of dependent loads, so
-// everything that does not come from the parts is found before the wait, and the partial
-// rows are requested together with their maxima.
-constexpr int kJoinWarps = 4;
-template <int HD>
-__global__ void __launch_bounds__(32 * kJoinWarps)
+// WPR warps per (token, head) row; warp w of a row takes the parts w, w + WPR, ..., and the
+// warps' sums are added in order (the result does not depend on timing).  A chain of
+// dependent loads, so everything that does not come from the parts is found before the wait,
+// and the partial rows are requested together with their maxima.  Four warps a row while the
+// rows are few (32 parts of 4 rows: 8 us with one warp, 2 us with four), one when they fill the
+// GPU by themselves (2664 rows of 10 parts: JOIN_ONE).
+constexpr int kJoinThreads = 128;
+template <int HD, int WPR>
+__global__ void __launch_bounds__(kJoinThreads)
     prompt_join_kernel(const __grid_constant__ Plan plan, const PParams p) {
-  constexpr int V = HD / 32, AHEAD = 4;
-  __shared__ float sh[kJoinWarps][HD + 2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = blockIdx.x;
+  constexpr int V = HD / 32, AHEAD = WPR == 1 ? 8 : 4, ROWS = kJoinThreads / 32 / WPR;
+  __shared__ float sh[WPR > 1 ? WPR : 1][HD + 2];
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % WPR;
+  const int total = plan.join0[plan.n];
+  const int r = blockIdx.x * ROWS + (threadIdx.x >> 5) / WPR;
+  const bool live = r < total;
   int lo = 0, hi = plan.n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -854,21 +519,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   }
   const int H = p.n_kv * p.group;
   const int64_t rows = (int64_t)plan.q_len[lo] * H;
-  const int parts = plan.parts[lo];
+  const int parts = live ? plan.parts[lo] : 0;
   const int rr = r - plan.join0[lo];
   const int64_t at = (int64_t)plan.part0[lo] + rr;
   const int tok = rr / H, head = rr - tok * H;
-  __nv_bfloat16* dst = p.o + (plan.q0[lo] + (int64_t)tok) * p.o_rs + head * p.o_hs;
+  __nv_bfloat16* dst = p.o + (plan.q0[lo] + (int64_t)tok) * p.o_rs + head * p.o_hs + lane * V;
   griddep_wait();
   griddep_trigger();
-  // this warp's parts, AHEAD at a time, each with a running maximum
+  // this warp's parts, AHEAD at a time, with a running maximum
   float m = -INFINITY, den = 0.f, acc[V] = {};
-  for (int s0 = warp; s0 < parts; s0 += AHEAD * kJoinWarps) {
+  for (int s0 = warp; s0 < parts; s0 += AHEAD * WPR) {
     float2 ml[AHEAD];
     float v[AHEAD][V];
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
-      const int s = s0 + j * kJoinWarps;
+      const int s = s0 + j * WPR;
       ml[j] = make_float2(-INFINITY, 0.f);
       if (s < parts) {
         const int64_t a = at + s * rows;
@@ -894,60 +559,59 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
       m = mn;
     }
   }
+  if constexpr (WPR > 1) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) sh[warp][lane * V + e] = acc[e];
-  if (lane == 0) {
-    sh[warp][HD] = m;
-    sh[warp][HD + 1] = den;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    float mm = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) mm = sh[w][HD + 1] == 0.f ? mm : fmaxf(mm, sh[w][HD]);
-    float d = 0.f, o[V] = {};
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      if (sh[w][HD + 1] == 0.f) continue;
-      const float f = ex2(sh[w][HD] - mm);
-      d = fmaf(sh[w][HD + 1], f, d);
-#pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = fmaf(sh[w][lane * V + e], f, o[e]);
+    for (int e = 0; e < V; ++e) sh[warp][lane * V + e] = acc[e];
+    if (lane == 0) {
+      sh[warp][HD] = m;
+      sh[warp][HD + 1] = den;
     }
-    const float inv = d == 0.f ? 0.f : 1.0f / d;
-    if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(dst + lane * V) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv),
-                                                             pack_bf16x2(o[2] * inv, o[3] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(dst + lane * V) = pack_bf16x2(o[0] * inv, o[1] * inv);
+    __syncthreads();
+    if (warp != 0) return;
+    m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) m = sh[w][HD + 1] == 0.f ? m : fmaxf(m, sh[w][HD]);
+    den = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      if (sh[w][HD + 1] == 0.f) continue;
+      const float f = ex2(sh[w][HD] - m);
+      den = fmaf(sh[w][HD + 1], f, den);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(sh[w][lane * V + e], f, acc[e]);
+    }
   }
+  if (!live) return;
+  const float inv = den == 0.f ? 0.f : 1.0f / den;
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
 }
 
-constexpr int kMinPart = 256;  // keys of a part at least
+constexpr double kL2Share = 48e6;  // bytes of keys and values that stay in L2 while their items run
 
-// Whether the wide kernel takes a call (see the table at make_plan).
-bool use_wide(int64_t ctas, int64_t keys_per_tile, int64_t sms) {
-  static const int f = getenv("ZDIT_WIDE") ? atoi(getenv("ZDIT_WIDE")) : -1;
-  if (f >= 0) return f;
-  return ctas >= sms && keys_per_tile >= 1024;
-}
-
-// Keys of a part: the length that gives the earliest end when the parts run over two slots
-// per SM, a part costing its keys plus kPartCost.
+// Keys of a part (INT_MAX: not split): the length that gives the earliest end when the parts
+// run over two slots per SM.  Costs in keys (0.01 us, what a key takes in a part of its own):
+// 400 for a part's set-up and output, 250 for the join and 6 for each part that it goes
+// through.  (One row group, head_dim 128, us split / not: 256 keys 7.1 / 6.9, 448 keys 6.2 / 9.1.)
 template <typename Seq>
-int64_t choose_part(const Seq* seq, int n, int tokens, int n_kv, int64_t sms) {
-  constexpr int64_t kPartCost = 512;
+int choose_part(const Seq* seq, int n, int tokens, int n_kv, int64_t sms) {
+  constexpr int kMinPart = 128, kPartCost = 400, kJoinCost = 250, kJoinPartCost = 6;
   const int64_t slots = 2 * sms;
-  int64_t longest = 1, items = 0, keys = 0;
+  int longest = 1;
+  int64_t items = 0;
   for (int i = 0; i < n; ++i) {
-    const int64_t t = (int64_t)((seq[i].ql + tokens - 1) / tokens) * n_kv;
-    longest = std::max<int64_t>(longest, seq[i].kl);
-    items += t;
-    keys += t * seq[i].kl;
+    longest = std::max(longest, seq[i].kl);
+    items += (int64_t)((seq[i].ql + tokens - 1) / tokens) * n_kv;
   }
   if (items >= slots || longest <= 2 * kMinPart) return INT_MAX;
-  int64_t best = INT_MAX, best_cost = longest + kPartCost / 2;  // not split: no join either
-  for (int c = kMinPart; c < longest; c += c / 4 / NTILE * NTILE) {
+  int64_t best_cost = (int64_t)longest + kPartCost;  // not split: no join either
+  int best = INT_MAX;
+  for (int c = kMinPart; c < longest; c += std::max(KTILE, c / 4 / KTILE * KTILE)) {
     int64_t m = 0;
     int big = 0;
     for (int i = 0; i < n; ++i) {
@@ -955,8 +619,7 @@ int64_t choose_part(const Seq* seq, int n, int tokens, int n_kv, int64_t sms) {
       m += (int64_t)((seq[i].ql + tokens - 1) / tokens) * n_kv * parts;
       big = std::max(big, (seq[i].kl + parts - 1) / parts);
     }
-    const int64_t waves = (m + slots - 1) / slots;
-    const int64_t cost = std::max(waves * (big + kPartCost), (keys + m * kPartCost) / slots + kPartCost);
+    const int64_t cost = (m + slots - 1) / slots * (big + kPartCost) + kJoinCost + kJoinPartCost * (longest / c);
     if (cost < best_cost) {
       best_cost = cost;
       best = c;
@@ -967,8 +630,7 @@ int64_t choose_part(const Seq* seq, int n, int tokens, int n_kv, int64_t sms) {
 
 struct HostPlan {
   Plan p;
-  bool wide;
-  int tokens, group;
+  int tokens, group, heads_at_once;
   int64_t q_rows, kv_rows, part_rows;
   double pairs;  // allowed (query, key) pairs, for the profiler
 };
@@ -985,9 +647,6 @@ bool make_plan(const zdit_prompt_attention_args& a, HostPlan* h) {
   Seq seq[kMaxSeqs];
   int n = 0;
   int64_t q = 0, kv = 0;
-  int64_t work = 0;   // keys over all one-tile items of a key head
-  int64_t tiles = 0;  // one-tile items of a key head
-  int64_t pairs = 0;  // two-tile items of a key head
   h->kv_rows = 0;
   h->pairs = 0;
   for (int b = 0; b < a.batch; ++b) {
@@ -1000,31 +659,29 @@ bool make_plan(const zdit_prompt_attention_args& a, HostPlan* h) {
       double seen = (double)ql * kl;  // allowed pairs
       if (a.causal) seen = kl >= ql ? seen - 0.5 * ql * (ql - 1.0) : 0.5 * kl * (kl + 1.0);
       h->pairs += seen;
-      tiles += (ql + h->tokens - 1) / h->tokens;
-      pairs += (ql + 2 * h->tokens - 1) / (2 * h->tokens);
-      work += (int64_t)(seen / h->tokens) + 1;
     }
     q += ql;
   }
   h->q_rows = q;
   const int64_t sms = num_sms();
-  h->wide = use_wide(pairs * a.n_kv_heads, n > 0 ? work / std::max<int64_t>(tiles, 1) : 0, sms);
   // Longest key range first: its items start early.
   std::sort(seq, seq + n, [](const Seq& x, const Seq& y) { return x.kl != y.kl ? x.kl > y.kl : x.q0 < y.q0; });
-  const int64_t part_keys = h->wide ? INT_MAX : choose_part(seq, n, h->tokens, a.n_kv_heads, sms);
+  const int part_keys = choose_part(seq, n, h->tokens, a.n_kv_heads, sms);
+  // key heads whose items run together: as many as keep the longest sequence's keys in L2
+  const double head_bytes = n > 0 ? 4.0 * a.head_dim * seq[0].kl : 0.0;
+  h->heads_at_once = head_bytes * a.n_kv_heads <= kL2Share ? a.n_kv_heads : std::max(1, (int)(kL2Share / head_bytes));
   int64_t items = 0, parts_rows = 0, join = 0;
   Plan& p = h->p;
   p.n = n;
   for (int i = 0; i < n; ++i) {
     const Seq& s = seq[i];
-    const int per = h->wide ? 2 * h->tokens : h->tokens;
-    const int parts = (int)std::max<int64_t>(1, (s.kl + part_keys - 1) / part_keys);
+    const int parts = part_keys == INT_MAX ? 1 : std::max(1, (s.kl + part_keys - 1) / part_keys);
     p.item0[i] = (int)items;
     p.q0[i] = s.q0; p.q_len[i] = s.ql; p.kv0[i] = s.kv0; p.kv_len[i] = s.kl; p.parts[i] = parts;
-    p.chunk[i] = ((s.kl + parts - 1) / parts + NTILE - 1) / NTILE * NTILE;  // parts of equal length
+    p.chunk[i] = ((s.kl + parts - 1) / parts + KTILE - 1) / KTILE * KTILE;  // parts of equal length
     p.part0[i] = (int)parts_rows;
     p.join0[i] = (int)join;
-    items += (int64_t)((s.ql + per - 1) / per) * parts;
+    items += (int64_t)((s.ql + h->tokens - 1) / h->tokens) * parts;
     if (parts > 1) {
       join += (int64_t)s.ql * a.n_heads;
       parts_rows += (int64_t)s.ql * a.n_heads * parts;
@@ -1051,27 +708,22 @@ zdit_status launch_prompt(const CUtensorMap& tq, const CUtensorMap& tk, const CU
     ProfScope ps(PROF_ATTENTION, 4.0 * HD * H * h.pairs,
                  2.0 * HD * (2.0 * H * h.q_rows + 2.0 * p.n_kv * h.kv_rows), s);
     const dim3 grid((unsigned)(h.p.item0[h.p.n] * p.n_kv));
-    // the shared-memory opt-in is set per launch: it belongs to the current context
-    if (h.wide) {
-      if (cudaFuncSetAttribute(prompt_attn_wide_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               Cfg<HD>::SMEM) != cudaSuccess ||
-          launch_dependent(prompt_attn_wide_kernel<HD>, grid, dim3(THREADS), Cfg<HD>::SMEM, s, tq, tk, tv, h.p, p) !=
-              cudaSuccess)
-        return ZDIT_ERR_CUDA;
-    } else if (cudaFuncSetAttribute(prompt_attn_narrow_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    NCfg<HD>::SMEM) != cudaSuccess ||
-               launch_dependent(prompt_attn_narrow_kernel<HD>, grid, dim3(NTHREADS), NCfg<HD>::SMEM, s, tq, tk, tv, h.p,
-                                p) != cudaSuccess) {
+    // per launch: the shared-memory opt-in belongs to the current context
+    if (cudaFuncSetAttribute(prompt_attn_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::SMEM) !=
+            cudaSuccess ||
+        launch_dependent(prompt_attn_kernel<HD>, grid, dim3(THREADS), Cfg<HD>::SMEM, s, tq, tk, tv, h.p, p) !=
+            cudaSuccess)
       return ZDIT_ERR_CUDA;
-    }
   }
   const int join = h.p.join0[h.p.n];
   if (join > 0) {
     ProfScope ps(PROF_ATTENTION, 0.0, (4.0 * HD + 8.0) * h.part_rows + 2.0 * HD * join, s);
-    if (launch_dependent(prompt_join_kernel<HD>, dim3((unsigned)join), dim3(32 * kJoinWarps), 0, s,
-                         h.p, p) !=
-        cudaSuccess)
-      return ZDIT_ERR_CUDA;
+    const dim3 block(kJoinThreads);
+    const cudaError_t e =
+        join > 8 * num_sms()
+            ? launch_dependent(prompt_join_kernel<HD, 1>, dim3((unsigned)((join + 3) / 4)), block, 0, s, h.p, p)
+            : launch_dependent(prompt_join_kernel<HD, 4>, dim3((unsigned)join), block, 0, s, h.p, p);
+    if (e != cudaSuccess) return ZDIT_ERR_CUDA;
   }
   return cudaGetLastError() == cudaSuccess ? ZDIT_OK : ZDIT_ERR_CUDA;
 }
@@ -1119,7 +771,7 @@ ZDIT_API zdit_status zdit_prompt_attention(const zdit_prompt_attention_args* a, 
   if (h.q_rows == 0) return ZDIT_OK;
   if (!device_ok()) return ZDIT_ERR_UNSUPPORTED;
   PParams p;
-  p.n_kv = a->n_kv_heads; p.group = h.group; p.tokens = h.tokens; p.causal = a->causal;
+  p.n_kv = a->n_kv_heads; p.group = h.group; p.tokens = h.tokens; p.heads_at_once = h.heads_at_once; p.causal = a->causal;
   const float scale = a->scale == 0.f ? 1.0f / sqrtf((float)a->head_dim) : a->scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.o = static_cast<__nv_bfloat16*>(a->o.ptr); p.o_rs = a->o.row_stride; p.o_hs = a->o.head_stride;
@@ -1128,16 +780,15 @@ ZDIT_API zdit_status zdit_prompt_attention(const zdit_prompt_attention_args* a, 
                                              ((size_t)h.part_rows * sizeof(float2) + 255) / 256 * 256) : nullptr;
   p.err = device_error_ptr();
   CUtensorMap tq, tk, tv;
-  const int key_box = h.wide ? TILE : NTILE;
   if (h.kv_rows == 0) {
     // no sequence has a key: no K or V tile is loaded, the maps only have to be valid
-    if (!make_tmap_bf16_heads(&tk, a->q.ptr, 1, 1, a->head_dim, a->head_dim, a->head_dim, 1, key_box))
+    if (!make_tmap_bf16_heads(&tk, a->q.ptr, 1, 1, a->head_dim, a->head_dim, a->head_dim, 1, KTILE))
       return ZDIT_ERR_CUDA;
     tv = tk;
   } else if (!make_tmap_bf16_heads(&tk, a->k.ptr, h.kv_rows, a->n_kv_heads, a->head_dim, a->k.row_stride,
-                                   a->k.head_stride, 1, key_box) ||
+                                   a->k.head_stride, 1, KTILE) ||
              !make_tmap_bf16_heads(&tv, a->v.ptr, h.kv_rows, a->n_kv_heads, a->head_dim, a->v.row_stride,
-                                   a->v.head_stride, 1, key_box)) {
+                                   a->v.head_stride, 1, KTILE)) {
     return ZDIT_ERR_CUDA;
   }
   if (!make_tmap_bf16_heads(&tq, a->q.ptr, h.q_rows, a->n_heads, a->head_dim, a->q.row_stride, a->q.head_stride,
