@@ -418,7 +418,7 @@ struct PairRing {
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + 256;
 };
 template <int EPI>
-__host__ __device__ constexpr int pair_bk() { return EPI == EPI_SWIGLU ? 128 : 64; }
+__host__ __device__ constexpr int pair_bk() { return EPI == EPI_SWIGLU || EPI == EPI_LINEAR ? 128 : 64; }
 
 template <int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
@@ -688,7 +688,7 @@ zdit_status launch_gemm(const GemmArgs& a, cudaStream_t s) {
   kp.rcos = a.rope_cos; kp.rsin = a.rope_sin; kp.qn = a.qn; kp.kn = a.kn; kp.eps = a.eps; kp.dim = a.dim;
   kp.num_m = pair ? (a.M + 255) / 256 : (a.M + BM - 1) / BM;
   kp.num_n = (a.N + BN - 1) / BN;
-  const int kslice = !pair ? BK : (a.epi == EPI_SWIGLU ? pair_bk<EPI_SWIGLU>() : pair_bk<EPI_BF16>());
+  const int kslice = !pair ? BK : (linear ? pair_bk<EPI_LINEAR>() : a.epi == EPI_SWIGLU ? pair_bk<EPI_SWIGLU>() : pair_bk<EPI_BF16>());
   kp.num_k = (a.K + kslice - 1) / kslice;
   // L2-aware raster: a band of tiles of one operand (about 32 MB, well inside one
   // die's share of the L2) stays resident while the other operand streams; the

@@ -3,15 +3,17 @@
 // Two kernels.  Many rows: the persistent projection GEMM of gemm.cu with the epilogue of
 // linear_epi.cuh.  Few rows: the kernel below, which is bound by streaming w once.  There
 // the weights are the 128-row operand of the tensor core and the rows of a its N side (16 to
-// 256 columns, a multiple of 16), so a tile computes 128 output features for all rows with
+// 160 columns, a multiple of 16), so a tile computes 128 output features for all rows with
 // no padding of M to 128, and N / 128 tiles times `split` parts of K spread the weights
 // over the SMs.  The parts of one tile are a cluster: each leaves its fp32 partial tile in
 // its own shared memory and every CTA adds up its share of the rows over the cluster's
 // shared memory, in rank order (the result does not depend on timing, and there is no
-// workspace to clear or share).
+// workspace to clear or share).  That traffic runs at ~2 TB/s over the GPU, so the more rows
+// the fewer parts; sending the rows to their owners with bulk copies instead is no faster
+// (133 x 9728 x 2560 19.3 against 18.0 us, 1 x 2560 x 4096 8.4 against 7.5).
 //
 // Warp roles (320 threads): warp 0 loads (TMA ring), warp 1 issues the MMAs, warps 2-9 move
-// the accumulator (TMEM lane = feature, column = row of a) to shared memory and finish.
+// the accumulator (TMEM lane = feature, column = row of a).
 #include <algorithm>
 #include <cmath>
 
@@ -31,6 +33,7 @@ constexpr int BK = 64;               // K slice
 constexpr int W_TILE = FT * BK * 2;  // 16 KB
 constexpr int EPI_WARPS = 8;         // two per TMEM lane group
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int kRing = 110 * 1024;    // shared memory of the ring: two CTAs fit an SM
 constexpr int kMaxStages = 8;
 constexpr int kMaxSplit = 8;         // portable cluster size
 constexpr int kMaxRowTile = 160;     // rows of a in one tile
@@ -47,6 +50,12 @@ struct FewParams {
   int* err;
 };
 
+__device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t cta) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
+  return r;
+}
+
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -55,10 +64,50 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t cta) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
-  return r;
+
+// 32 lanes x 8 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr));
+}
+
+// Adds the residual to and stores n <= 8 rows of one feature: element offsets res and out, a
+// row further each.  Types are told apart outside the loops and addresses advance by a row:
+// with one value a lane and row, every instruction here counts.
+template <typename T>
+__device__ __forceinline__ void add_rows(const T* p, int64_t step, int n, float (&v)[8]) {
+  T t[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j, p += step)
+    if (j < n) t[j] = *p;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) v[j] += static_cast<float>(t[j]);
+}
+template <typename T>
+__device__ __forceinline__ void store_rows(T* p, int64_t step, int n, const float (&v)[8]) {
+  if (n == 8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j, p += step) *p = static_cast<T>(v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j, p += step)
+      if (j < n) *p = static_cast<T>(v[j]);
+  }
+}
+__device__ __forceinline__ void finish_rows(const LinearEpi& e, int64_t res, int64_t out, int n, float (&v)[8]) {
+  if (e.residual != nullptr) {
+    if (e.res_f32)
+      add_rows(static_cast<const float*>(e.residual) + res, e.ld_res, n, v);
+    else
+      add_rows(static_cast<const __nv_bfloat16*>(e.residual) + res, e.ld_res, n, v);
+  }
+  if (e.out_f32)
+    store_rows(static_cast<float*>(e.out) + out, e.ld_out, n, v);
+  else
+    store_rows(static_cast<__nv_bfloat16*>(e.out) + out, e.ld_out, n, v);
 }
 
 __global__ void __launch_bounds__(THREADS)
@@ -165,59 +214,81 @@ __global__ void __launch_bounds__(THREADS)
     mbar_wait(done, 0, &dummy);
   }
   __syncthreads();  // (the other warps wait here, not in a polling loop)
-  // The partial tile, [row][128 features] fp32, over the idle ring.
-  float* part = reinterpret_cast<float*>(smem);
   const int rows = min(p.row_tile, p.M - r0);
-  if (warp >= 2) {
-    tc_fence_after();
-    if (!abort_flag) {
-      const int lg = warp & 3;
-      const uint32_t t0 = tmem + ((uint32_t)(lg * 32) << 16);
-      float* col = part + lg * 32 + lane;
-      for (int c = (warp - 2) / 4 * 16; c < rows; c += 32) {
-        uint32_t r[16];
-        tmem_ld16(t0 + c, r);
+  const int lg = warp & 3, half = (warp - 2) >> 2;  // TMEM lane group; which of its two warps
+  const uint32_t t0 = tmem + ((uint32_t)(lg * 32) << 16);
+  if (p.split == 1) {
+    // straight from the accumulator, 8 rows of one feature per lane at a time
+    if (warp >= 2 && !abort_flag) {
+      tc_fence_after();
+      const int f = f0 + lg * 32 + lane;
+      const bool f_ok = f < p.N;
+      const float bias = p.e.bias != nullptr && f_ok ? __ldg(p.e.bias + f) : 0.f;
+      for (int c = half * 8; c < rows; c += 16) {
+        uint32_t t[8];
+        __syncwarp();
+        tmem_ld8(t0 + c, t);
         tmem_ld_wait();
+        float v[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) col[(c + j) * FT] = __uint_as_float(r[j]);
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(t[j]) + bias;
+        linear_act_all<8>(v, p.e.act);
+        const int64_t row = r0 + c;
+        if (f_ok) finish_rows(p.e, row * p.e.ld_res + f, row * p.e.ld_out + f, min(8, rows - c), v);
       }
     }
     tc_fence_before();
-  }
-  __syncwarp();
-  cluster_sync();  // partial tiles of the whole cluster are visible
-  if (warp >= 2 && !abort_flag) {
-    // rows rank, rank + split, ... of the tile: a warp adds up kRows of them at a time, 4
-    // features per lane, all loads of the cluster in flight at once
-    const int f = f0 + lane * 4;
-    const uint32_t base = smem_u32(part) + lane * 16;
-    constexpr int kRows = 2;
-    const int step = EPI_WARPS * p.split;
-    uint32_t peer[kMaxSplit];
+    __syncthreads();
+  } else {
+    // the partial tile, [row][128 features] fp32, over the idle ring
+    float* part = reinterpret_cast<float*>(smem);
+    if (warp >= 2 && !abort_flag) {
+      tc_fence_after();
+      float* col = part + lg * 32 + lane;
+      for (int c = half * 8; c < rows; c += 16) {
+        uint32_t t[8];
+        tmem_ld8(t0 + c, t);
+        tmem_ld_wait();
 #pragma unroll
-    for (int s = 0; s < kMaxSplit; ++s) peer[s] = map_cluster(base, s < p.split ? s : rank);
-    for (int r = rank + (warp - 2) * p.split; r < rows; r += kRows * step) {
-      float4 q[kRows][kMaxSplit];
-#pragma unroll
-      for (int i = 0; i < kRows; ++i)
-#pragma unroll
-        for (int s = 0; s < kMaxSplit; ++s)
-          q[i][s] = s < p.split && r + i * step < rows ? ld_cluster_f4(peer[s] + (r + i * step) * (FT * 4))
-                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        if (r + i * step >= rows) break;
-        float v[4] = {q[i][0].x, q[i][0].y, q[i][0].z, q[i][0].w};
-#pragma unroll
-        for (int s = 1; s < kMaxSplit; ++s) {
-          v[0] += q[i][s].x; v[1] += q[i][s].y; v[2] += q[i][s].z; v[3] += q[i][s].w;
-        }
-        linear_finish<4>(p.e, r0 + r + i * step, f, p.N, v);
+        for (int j = 0; j < 8; ++j) col[(c + j) * FT] = __uint_as_float(t[j]);
       }
     }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();  // partial tiles of the whole cluster are visible
+    if (warp >= 2 && !abort_flag) {
+      // rows rank, rank + split, ... of the tile: a warp adds up kRows of them at a time, 4
+      // features per lane, all loads of the cluster in flight at once
+      const int f = f0 + lane * 4;
+      const uint32_t base = smem_u32(part) + lane * 16;
+      constexpr int kRows = 2;
+      const int step = EPI_WARPS * p.split;
+      uint32_t peer[kMaxSplit];
+#pragma unroll
+      for (int s = 0; s < kMaxSplit; ++s) peer[s] = map_cluster(base, s < p.split ? s : rank);
+      for (int r = rank + (warp - 2) * p.split; r < rows; r += kRows * step) {
+        float4 q[kRows][kMaxSplit];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+          for (int s = 0; s < kMaxSplit; ++s)
+            q[i][s] = s < p.split && r + i * step < rows ? ld_cluster_f4(peer[s] + (r + i * step) * (FT * 4))
+                                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          if (r + i * step >= rows) break;
+          float v[4] = {q[i][0].x, q[i][0].y, q[i][0].z, q[i][0].w};
+#pragma unroll
+          for (int s = 1; s < kMaxSplit; ++s) {
+            v[0] += q[i][s].x; v[1] += q[i][s].y; v[2] += q[i][s].z; v[3] += q[i][s].w;
+          }
+          linear_finish<4>(p.e, r0 + r + i * step, f, p.N, v);
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while a peer may still read its tile
   }
-  __syncwarp();
-  cluster_sync();  // no CTA leaves while a peer may still read its tile
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, p.tmem_cols);
@@ -261,8 +332,8 @@ bool plan_few(int64_t M, int64_t N, int64_t K, FewPlan* f) {
   // the row tile takes its share of the ring.  Two CTAs fit an SM.
   f->group = f->row_tile <= 32 ? 2 : 1;
   const int stage = f->group * (W_TILE + f->row_tile * BK * 2);
-  f->stages = std::min(110 * 1024 / stage, kMaxStages);
-  f->smem = 1024 + std::max(f->stages * stage, f->row_tile * FT * 4);
+  f->stages = std::min(kRing / stage, kMaxStages);
+  f->smem = 1024 + std::max(f->stages * stage, f->split > 1 ? f->row_tile * FT * 4 : 0);
   f->tmem_cols = 32;
   while (f->tmem_cols < (uint32_t)f->row_tile) f->tmem_cols *= 2;
   return true;
