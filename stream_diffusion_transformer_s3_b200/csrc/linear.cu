@@ -301,35 +301,41 @@ struct FewPlan {
   uint32_t tmem_cols;
 };
 
-// Whether the few-row kernel takes a problem, and how.  us at N x K, M rows, this kernel
-// against the projection GEMM (bf16 out, SiLU, weights cold):
-//   2560 x 4096   M 16  8 / 31   M 133 16 / 32   M 512 20 / 27   M 1024 41 / 30
-//   9728 x 2560   M 16 13 / 24   M 133 19 / 25   M 200 29 / 25   M 512  57 / 35
-//   3840 x 10240  M 16 18 / 69   M 133 25 / 69   M 512 48 / 56   M 1024 86 / 62
-// i.e. up to 160 rows (one tile of them), and beyond that while the tiles alone (128 features
-// x up to 128 rows) do not give the GEMM's 256-wide tiles a GPU's worth of work.
+// Whether the few-row kernel takes a problem, and how.  Expected times in us, fitted to the
+// measured ones (within ~15%) over N x K of 500 x 5000 to 9728 x 2560 and 1 to 1024 rows:
+//   few rows   3.0 + slices per part * (0.30 + 0.0012 row_tile) * load
+//              (or the time to read w at 6.6 TB/s, if that is more) + the finish: 0.018 a row
+//              unsplit, else 0.8 + 0.04 a row and CTA on the SM (the cluster's shared memory)
+//              load: 1 up to one CTA per SM, 1.2 up to 1.6 (two CTAs fill each other's gaps)
+//   GEMM       10 + 0.27 a slice and wave of its 256-wide tiles
+// e.g. us few rows / GEMM at 2560 x 4096: 16 rows 8 / 31, 133 rows 15 / 32, 512 rows 20 / 27;
+// 9728 x 2560: 13 / 24, 18 / 25, 57 / 35; 3840 x 10240: 16 / 69, 24 / 69, 48 / 56.
+// Clusters of 5 to 7 pack badly into the GPCs (6144 x 2560, 1 row: 6 parts 16.6 us, 3 parts 9.9).
 bool plan_few(int64_t M, int64_t N, int64_t K, FewPlan* f) {
+  const double sms = num_sms(), slices = (double)((K + BK - 1) / BK);
+  const double wide_tiles = (double)(M > 256 ? (M + 255) / 256 : (M + 127) / 128) * ((N + 255) / 256);
+  const double gemm = 10.0 + 0.27 * slices * std::ceil(wide_tiles / (M > 256 ? sms / 2 : sms));
   const int64_t row_tiles = M <= kMaxRowTile ? 1 : (M + 127) / 128;
-  const int64_t tiles = (N + FT - 1) / FT * row_tiles;
-  const int sms = num_sms();
-  if (row_tiles > 1 && tiles * 5 > (int64_t)sms * 4) return false;
+  const double tiles = (double)((N + FT - 1) / FT) * row_tiles;
   f->row_tiles = (int)row_tiles;
   f->row_tile = (int)(((M + row_tiles - 1) / row_tiles + 15) / 16 * 16);
-  // Parts of K: about one CTA per SM; past half a GPU of tiles up to 1.6 per SM, because two
-  // CTAs on an SM hide each other's pipeline bubbles (9728 x 2560, 133 rows: 3 parts 18.9 us,
-  // 2 parts 21.5).  Clusters of 5 to 7 pack badly into the GPCs (6144 x 2560, 1 row: 6 parts
-  // 16.6 us, 3 parts 9.9).  At least 4 slices a part.
-  const int64_t slices = (K + BK - 1) / BK;
-  const int sizes[] = {8, 4, 3, 2, 1};
+  f->split = 0;
+  double best = gemm;
+  const int sizes[] = {1, 2, 3, 4, 8};
   for (const int s : sizes) {
-    f->split = s;
-    if (s == 1) break;
-    if (slices / s < 4) continue;
-    if (tiles * s * 10 <= (int64_t)sms * 11) break;
-    if (tiles * 2 >= sms && tiles * s * 10 <= (int64_t)sms * 16 + 40) break;
+    const double ctas = tiles * s / sms;  // per SM
+    if (ctas > 1.63 || (s > 1 && slices < 2 * s)) break;
+    const double stream = std::max(std::ceil(slices / s) * (0.30 + 0.0012 * f->row_tile) * (ctas <= 1 ? 1.0 : 1.2),
+                                   2.0 * N * K / 6.6e6);
+    const double finish = s == 1 ? 0.018 * f->row_tile : 0.8 + 0.04 * f->row_tile * std::max(1.0, ctas);
+    if (3.0 + stream + finish < best) {
+      best = 3.0 + stream + finish;
+      f->split = s;
+    }
   }
+  if (f->split == 0) return false;
   // Two slices per stage while the rows are few (fewer waits: 1 row 7.9 -> 7.5 us); one when
-  // the row tile takes its share of the ring.  Two CTAs fit an SM.
+  // the row tile takes its share of the ring.
   f->group = f->row_tile <= 32 ? 2 : 1;
   const int stage = f->group * (W_TILE + f->row_tile * BK * 2);
   f->stages = std::min(kRing / stage, kMaxStages);
