@@ -398,11 +398,17 @@ def _dtype_code(t, where):
     raise ValueError(f"{where}: {dt} is neither bfloat16 nor float32")
 
 
-def _on_device(where, *tensors):
-    dev = _th().cuda.current_device()
+def _launch_stream(where, stream, *tensors):
+    """Handle of the stream to launch on; the tensors must be on the current device."""
+    T = _th()
+    dev = T.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{where}: tensor on {t.device}, current device is cuda:{dev}")
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(T._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw is not None else T.cuda.current_stream().cuda_stream
 
 
 def _f32(where, name, t, *shape):
@@ -431,12 +437,11 @@ def zdit_rope_table_scaled(pos, rotary_dim, theta, cos_out, sin_out, scaling: Ro
         raise ValueError(f"{w}: pos must be a contiguous int32 vector")
     T = pos.shape[0]
     pc, ps = _f32(w, "cos_out", cos_out, T, rotary_dim // 2), _f32(w, "sin_out", sin_out, T, rotary_dim // 2)
-    _on_device(w, pos, cos_out, sin_out)
+    s = _launch_stream(w, stream, pos, cos_out, sin_out)
     if T == 0:
         return
     _check(lib().zdit_rope_table_scaled(pos.data_ptr(), T, rotary_dim, theta,
-                                        C.byref(scaling) if scaling is not None else None, pc, ps,
-                                        _stream(stream)), w)
+                                        C.byref(scaling) if scaling is not None else None, pc, ps, s), w)
 
 
 def zdit_qk_norm_rope(q, k, q_out, k_out, w_q, w_k, cos, sin, rotary_dim, layout=ROPE_HALF, eps=1e-6, stream=None):
@@ -462,10 +467,10 @@ def zdit_qk_norm_rope(q, k, q_out, k_out, w_q, w_k, cos, sin, rotary_dim, layout
         pc, ps = _f32(w, "cos", cos, T, rotary_dim // 2), _f32(w, "sin", sin, T, rotary_dim // 2)
     a = _qk_args(T, n_q, n_k, hd, _dtype_code(q, w), _dtype_code(q_out, w), *hq, *hk, *hqo, *hko, pq, pk, eps, pc, ps,
                  rotary_dim, layout)
-    _on_device(w, q, k, q_out, k_out, w_q, w_k, cos, sin)
+    s = _launch_stream(w, stream, q, k, q_out, k_out, w_q, w_k, cos, sin)
     if T == 0:
         return
-    _check(lib().zdit_qk_norm_rope(C.byref(a), _stream(stream)), w)
+    _check(lib().zdit_qk_norm_rope(C.byref(a), s), w)
 
 
 class PromptBatch:
@@ -508,10 +513,10 @@ def zdit_prompt_attention(q, k, v, o, batch: PromptBatch, workspace=None, causal
     hk, hv = _heads(w, "k", k, (S, Hkv, hd)), _heads(w, "v", v, (S, Hkv, hd))
     if R < batch.q_rows or o.shape[0] < batch.q_rows or S < batch.kv_rows:
         raise ValueError(f"{w}: the batch needs {batch.q_rows} rows of q and o and {batch.kv_rows} of k and v")
-    _on_device(w, q, k, v, o, workspace)
+    s = _launch_stream(w, stream, q, k, v, o, workspace)
     a = batch.args(H, Hkv, hd, causal, scale, hq + hk + hv + ho)
     pw, nw = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _check(lib().zdit_prompt_attention(C.byref(a), pw, nw, _stream(stream)), w)
+    _check(lib().zdit_prompt_attention(C.byref(a), pw, nw, s), w)
 
 
 def zdit_linear(a, w, out, bias=None, act=ACT_NONE, residual=None, stream=None):
@@ -534,10 +539,10 @@ def zdit_linear(a, w, out, bias=None, act=ACT_NONE, residual=None, stream=None):
             raise ValueError(f"{n}: residual must be [{M}, {N}] with contiguous rows")
     g = _linear_args(M, N, K, a.data_ptr(), lda, w.data_ptr(), ldw, _f32(n, "bias", bias, N), act, pr, ldr, dr,
                      out.data_ptr(), ldo, _dtype_code(out, n))
-    _on_device(n, a, w, out, bias, residual)
+    s = _launch_stream(n, stream, a, w, out, bias, residual)
     if M == 0:
         return
-    _check(lib().zdit_linear(C.byref(g), _stream(stream)), n)
+    _check(lib().zdit_linear(C.byref(g), s), n)
 
 
 # ------------------------------------------------------------------------ stack

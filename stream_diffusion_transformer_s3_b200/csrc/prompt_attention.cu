@@ -58,6 +58,7 @@ struct Plan {
   int n;  // sequences with query rows
   int item0[kMaxSeqs + 1];  // first item (per key head) of sequence i; item0[n] = all
   int q0[kMaxSeqs], q_len[kMaxSeqs], kv0[kMaxSeqs], kv_len[kMaxSeqs];
+  int tiles[kMaxSeqs];      // query tiles
   int parts[kMaxSeqs];      // key splits
   int chunk[kMaxSeqs];      // keys of a part, a multiple of KTILE
   int part0[kMaxSeqs];      // first partial row of the sequence in the workspace (parts > 1)
@@ -66,8 +67,8 @@ struct Plan {
 
 struct PParams {
   int n_kv, group, tokens;  // tokens per query tile
-  int heads_at_once;        // key heads whose items are interleaved
   int causal;
+  int heads_first;          // grid (key heads, items) instead of (items, key heads)
   float scale_log2;
   __nv_bfloat16* o;
   int64_t o_rs, o_hs;
@@ -248,7 +249,43 @@ __global__ void __launch_bounds__(THREADS, 2)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
+
+  // Item of this CTA: the items of a head come by decreasing work, either head after head or
+  // all heads of an item next to each other (see launch_prompt).  No division on the way to
+  // the first load unless keys are split.
+  const int kvh = p.heads_first ? blockIdx.x : blockIdx.y;
+  const int item = p.heads_first ? blockIdx.y : blockIdx.x;
+  const int sq = find_item(plan, item);
+  const int q_len = plan.q_len[sq], kv_len = plan.kv_len[sq], kv0 = plan.kv0[sq], q0 = plan.q0[sq];
+  const int parts = plan.parts[sq];
+  int tile = item - plan.item0[sq], part = 0, key_first = 0;
+  if (parts > 1) {
+    const int t = tile / parts;
+    part = tile - t * parts;
+    tile = t;
+    key_first = part * plan.chunk[sq];
+  }
+  const int tok0 = (plan.tiles[sq] - 1 - tile) * p.tokens;  // later rows see more keys: first
+  int n;  // key tiles of this item
+  {
+    const int lk = last_key(min(tok0 + p.tokens, q_len) - 1, q_len, kv_len, p.causal);
+    const int end = parts > 1 ? min(lk + 1, key_first + plan.chunk[sq]) : lk + 1;
+    n = end > key_first ? (end - key_first + KTILE - 1) / KTILE : 0;
+  }
+  auto load_k = [&](int i) {
+    uint8_t* sK = smem + C::OFF_K + (i % ST) * C::TILE_BYTES;
+    mbar_arrive_expect_tx(&k_full[i % ST], C::TILE_BYTES);
+    for (int c = 0; c < HD / 64; ++c)
+      tma_load_3d(sK + c * C::HALF, &tmK, &k_full[i % ST], c * 64, kvh, kv0 + key_first + i * KTILE);
+  };
+  auto load_v = [&](int i) {
+    uint8_t* sV = smem + C::OFF_V + (i % ST) * C::TILE_BYTES;
+    mbar_arrive_expect_tx(&v_full[i % ST], C::TILE_BYTES);
+    for (int c = 0; c < HD / 64; ++c)
+      tma_load_3d(sV + c * C::HALF, &tmV, &v_full[i % ST], c * 64, kvh, kv0 + key_first + i * KTILE);
+  };
+
+  if (warp == WARP_QK && lane == 0) {
     mbar_init(q_full, 1);
     mbar_init(pv_done, 1);
     mbar_init(mma_done, 1);
@@ -264,59 +301,33 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
     *abort_flag = 0;
     fence_barrier_init();
+    griddep_wait();  // Q, K, V of the predecessor are complete
+    // this thread made the barriers: its first loads need not wait for the others
+    if (n > 0) {
+      mbar_arrive_expect_tx(q_full, (uint32_t)(p.group * p.tokens * 128 * (HD / 64)));
+      for (int c = 0; c < HD / 64; ++c)
+        tma_load_3d(smem + c * C::Q_HALF, &tmQ, q_full, c * 64, kvh * p.group, q0 + tok0);
+      for (int i = 0; i < min(n, ST); ++i) load_k(i);
+      for (int i = 0; i < min(n, ST); ++i) load_v(i);
+    }
   }
-  if (warp == WARP_QK && lane == 0) {
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmK);
-  }
-  if (warp == WARP_V && lane == 0) tma_prefetch_desc(&tmV);
   if (warp == WARP_MMA) tmem_alloc(tmem_slot, 256);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-
-  // Items are ordered by groups of heads_at_once key heads (whose keys fit the L2 cache
-  // together), in a group by decreasing work, the heads of one item next to each other.
-  const int per_group = plan.item0[plan.n] * p.heads_at_once;
-  const int hg = blockIdx.x / per_group, in_group = blockIdx.x - hg * per_group;
-  const int heads = min(p.heads_at_once, p.n_kv - hg * p.heads_at_once);
-  const int item = in_group / heads;
-  const int kvh = hg * p.heads_at_once + in_group - item * heads;
-  const int sq = find_item(plan, item);
-  const int rem = item - plan.item0[sq];
-  const int q_len = plan.q_len[sq], kv_len = plan.kv_len[sq], kv0 = plan.kv0[sq], q0 = plan.q0[sq];
-  const int parts = plan.parts[sq], chunk = plan.chunk[sq];
-  const int n_tiles = (q_len + p.tokens - 1) / p.tokens;
-  const int part = rem % parts;
-  const int tok0 = (n_tiles - 1 - rem / parts) * p.tokens;  // later rows see more keys: first
-  const int key_first = part * chunk;
-  int n;  // key tiles of this item
-  {
-    const int lk = last_key(min(tok0 + p.tokens, q_len) - 1, q_len, kv_len, p.causal);
-    const int end = parts > 1 ? min(lk + 1, key_first + chunk) : lk + 1;
-    n = end > key_first ? (end - key_first + KTILE - 1) / KTILE : 0;
-  }
-  griddep_wait();     // Q, K, V of the predecessor are complete, the workspace is free
+  griddep_wait();     // (every thread: the outputs and the workspace are free)
   griddep_trigger();  // every CTA has started: the successor may launch
 
   if (warp == WARP_QK) {
-    if (lane == 0 && n > 0) {
+    if (lane == 0) {
       // ------------------------------------------------------------ Q and K
-      mbar_arrive_expect_tx(q_full, (uint32_t)(p.group * p.tokens * 128 * (HD / 64)));
-      for (int c = 0; c < HD / 64; ++c)
-        tma_load_3d(smem + c * C::Q_HALF, &tmQ, q_full, c * 64, kvh * p.group, q0 + tok0);
-      int issued = 0;
-      for (int i = 0; i < n; ++i) {
-        const int st = i % ST;
-        if (!mbar_wait(&k_empty[st], ((i / ST) & 1) ^ 1, abort_flag, p.err)) break;
-        uint8_t* sK = smem + C::OFF_K + st * C::TILE_BYTES;
-        mbar_arrive_expect_tx(&k_full[st], C::TILE_BYTES);
-        for (int c = 0; c < HD / 64; ++c)
-          tma_load_3d(sK + c * C::HALF, &tmK, &k_full[st], c * 64, kvh, kv0 + key_first + i * KTILE);
-        ++issued;
+      int issued = min(n, ST);
+      for (; issued < n; ++issued) {
+        if (!mbar_wait(&k_empty[issued % ST], ((issued / ST) & 1) ^ 1, abort_flag, p.err)) break;
+        load_k(issued);
       }
-      if (*abort_flag) {  // let copies in flight land before shared memory is released
+      if (*abort_flag && n > 0) {  // let copies in flight land before shared memory is released
         int dummy = 0;
         mbar_wait(q_full, 0, &dummy);
         for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(&k_full[i % ST], (i / ST) & 1, &dummy);
@@ -325,15 +336,10 @@ __global__ void __launch_bounds__(THREADS, 2)
   } else if (warp == WARP_V) {
     if (lane == 0) {
       // ------------------------------------------------------------ V
-      int issued = 0;
-      for (int i = 0; i < n; ++i) {
-        const int st = i % ST;
-        if (!mbar_wait(&v_empty[st], ((i / ST) & 1) ^ 1, abort_flag, p.err)) break;
-        uint8_t* sV = smem + C::OFF_V + st * C::TILE_BYTES;
-        mbar_arrive_expect_tx(&v_full[st], C::TILE_BYTES);
-        for (int c = 0; c < HD / 64; ++c)
-          tma_load_3d(sV + c * C::HALF, &tmV, &v_full[st], c * 64, kvh, kv0 + key_first + i * KTILE);
-        ++issued;
+      int issued = min(n, ST);
+      for (; issued < n; ++issued) {
+        if (!mbar_wait(&v_empty[issued % ST], ((issued / ST) & 1) ^ 1, abort_flag, p.err)) break;
+        load_v(issued);
       }
       if (*abort_flag) {
         int dummy = 0;
@@ -592,8 +598,6 @@ __global__ void __launch_bounds__(kJoinThreads)
     *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
 }
 
-constexpr double kL2Share = 48e6;  // bytes of keys and values that stay in L2 while their items run
-
 // Keys of a part (INT_MAX: not split): the length that gives the earliest end when the parts
 // run over two slots per SM.  Costs in keys (0.01 us, what a key takes in a part of its own):
 // 400 for a part's set-up and output, 250 for the join and 6 for each part that it goes
@@ -630,7 +634,7 @@ int choose_part(const Seq* seq, int n, int tokens, int n_kv, int64_t sms) {
 
 struct HostPlan {
   Plan p;
-  int tokens, group, heads_at_once;
+  int tokens, group;
   int64_t q_rows, kv_rows, part_rows;
   double pairs;  // allowed (query, key) pairs, for the profiler
 };
@@ -639,7 +643,7 @@ struct HostPlan {
 bool make_plan(const zdit_prompt_attention_args& a, HostPlan* h) {
   if (a.batch <= 0 || a.batch > kMaxSeqs || !a.q_len || a.n_kv_heads <= 0 || a.n_heads <= 0 ||
       a.n_heads % a.n_kv_heads || a.n_heads / a.n_kv_heads > 64 || (a.head_dim != 64 && a.head_dim != 128) ||
-      a.n_heads > (1 << 16) || a.causal < 0 || a.causal > 1)
+      a.n_heads > 65535 || a.causal < 0 || a.causal > 1)
     return false;
   h->group = a.n_heads / a.n_kv_heads;
   h->tokens = TILE / h->group;
@@ -667,9 +671,6 @@ bool make_plan(const zdit_prompt_attention_args& a, HostPlan* h) {
   // Longest key range first: its items start early.
   std::sort(seq, seq + n, [](const Seq& x, const Seq& y) { return x.kl != y.kl ? x.kl > y.kl : x.q0 < y.q0; });
   const int part_keys = choose_part(seq, n, h->tokens, a.n_kv_heads, sms);
-  // key heads whose items run together: as many as keep the longest sequence's keys in L2
-  const double head_bytes = n > 0 ? 4.0 * a.head_dim * seq[0].kl : 0.0;
-  h->heads_at_once = head_bytes * a.n_kv_heads <= kL2Share ? a.n_kv_heads : std::max(1, (int)(kL2Share / head_bytes));
   int64_t items = 0, parts_rows = 0, join = 0;
   Plan& p = h->p;
   p.n = n;
@@ -677,16 +678,17 @@ bool make_plan(const zdit_prompt_attention_args& a, HostPlan* h) {
     const Seq& s = seq[i];
     const int parts = part_keys == INT_MAX ? 1 : std::max(1, (s.kl + part_keys - 1) / part_keys);
     p.item0[i] = (int)items;
+    p.tiles[i] = (s.ql + h->tokens - 1) / h->tokens;
     p.q0[i] = s.q0; p.q_len[i] = s.ql; p.kv0[i] = s.kv0; p.kv_len[i] = s.kl; p.parts[i] = parts;
     p.chunk[i] = ((s.kl + parts - 1) / parts + KTILE - 1) / KTILE * KTILE;  // parts of equal length
     p.part0[i] = (int)parts_rows;
     p.join0[i] = (int)join;
-    items += (int64_t)((s.ql + h->tokens - 1) / h->tokens) * parts;
+    items += (int64_t)p.tiles[i] * parts;
     if (parts > 1) {
       join += (int64_t)s.ql * a.n_heads;
       parts_rows += (int64_t)s.ql * a.n_heads * parts;
     }
-    if (items * a.n_kv_heads > INT_MAX || parts_rows > INT_MAX || join > INT_MAX) return false;
+    if (items > INT_MAX || parts_rows > INT_MAX || join > INT_MAX) return false;
   }
   p.item0[n] = (int)items;
   p.join0[n] = (int)join;
@@ -702,12 +704,18 @@ size_t plan_bytes(const HostPlan& h, int head_dim) {
 
 template <int HD>
 zdit_status launch_prompt(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const HostPlan& h,
-                          const PParams& p, cudaStream_t s) {
+                          PParams p, cudaStream_t s) {
   const int H = p.n_kv * p.group;
   {
     ProfScope ps(PROF_ATTENTION, 4.0 * HD * H * h.pairs,
                  2.0 * HD * (2.0 * H * h.q_rows + 2.0 * p.n_kv * h.kv_rows), s);
-    const dim3 grid((unsigned)(h.p.item0[h.p.n] * p.n_kv));
+    // Head after head keeps one head's keys in L2 while its items run (30 heads, 16 prompts of
+    // 300 tokens: 47 against 57 us); but with few waves the last head's longest items would end
+    // the launch alone, so then the longest items of all heads come first (8 heads, 2 prompts of
+    // 1024 tokens: 24 against 32 us).  Unmasked items are all alike.
+    const int64_t items = h.p.item0[h.p.n];
+    p.heads_first = p.causal && items * p.n_kv < 9 * (int64_t)num_sms();
+    const dim3 grid = p.heads_first ? dim3((unsigned)p.n_kv, (unsigned)items) : dim3((unsigned)items, (unsigned)p.n_kv);
     // per launch: the shared-memory opt-in belongs to the current context
     if (cudaFuncSetAttribute(prompt_attn_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::SMEM) !=
             cudaSuccess ||
@@ -771,7 +779,7 @@ ZDIT_API zdit_status zdit_prompt_attention(const zdit_prompt_attention_args* a, 
   if (h.q_rows == 0) return ZDIT_OK;
   if (!device_ok()) return ZDIT_ERR_UNSUPPORTED;
   PParams p;
-  p.n_kv = a->n_kv_heads; p.group = h.group; p.tokens = h.tokens; p.heads_at_once = h.heads_at_once; p.causal = a->causal;
+  p.n_kv = a->n_kv_heads; p.group = h.group; p.tokens = h.tokens; p.causal = a->causal;
   const float scale = a->scale == 0.f ? 1.0f / sqrtf((float)a->head_dim) : a->scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.o = static_cast<__nv_bfloat16*>(a->o.ptr); p.o_rs = a->o.row_stride; p.o_hs = a->o.head_stride;
