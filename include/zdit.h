@@ -460,10 +460,9 @@ ZDIT_API zdit_status zdit_qk_norm_rope(const zdit_qk_norm_rope_args* a, void* st
  * no key is allowed for (q_len > kv_len, kv_len == 0) becomes zeros.
  *   q, o   bf16, sum(q_len) rows of n_heads; o does not overlap q, k or v; rows of o past
  *          the last sequence are not written
- *   k, v   bf16, n_kv_heads; sequences may share rows or leave gaps; rows of no sequence
- *          are never used, whatever they hold (NaN included).  Rows that a sequence does
- *          own have to hold finite values: keys are taken 128 at a time, so an infinity or
- *          NaN in a row of v reaches query rows of the same sequence that come before it.
+ *   k, v   bf16, n_kv_heads; sequences may share rows or leave gaps.  A row of k or v
+ *          reaches the query rows that it is allowed for and no others, whatever it holds
+ *          (infinities and NaN included); rows of no sequence are never used.
  *   q_len, kv_len, kv_start  HOST int32 [batch], read during the call only, values >= 0.
  *          kv_len NULL: q_len; kv_start NULL: sequences packed one after the other.
  *          A captured launch keeps the lengths it was captured with.

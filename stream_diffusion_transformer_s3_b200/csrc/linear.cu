@@ -401,6 +401,8 @@ ZDIT_API zdit_status zdit_linear(const zdit_linear_args* a, void* stream) {
   if (((reinterpret_cast<uintptr_t>(a->a) | reinterpret_cast<uintptr_t>(a->w)) & 15) || a->lda % 8 || a->ldw % 8)
     return ZDIT_ERR_ALIGNMENT;
   if ((reinterpret_cast<uintptr_t>(a->bias) & 3) || oa % oe || (a->residual && ra % re)) return ZDIT_ERR_ALIGNMENT;
+  if (a->residual == a->out && (oe != re || (a->M > 1 && a->ld_residual != a->ld_out))) return ZDIT_ERR_INVALID_ARG;
+  if (a->a == a->out || a->w == a->out) return ZDIT_ERR_INVALID_ARG;
   if (!device_ok()) return ZDIT_ERR_UNSUPPORTED;
   LinearEpi e{};
   e.bias = a->bias; e.residual = a->residual; e.out = a->out; e.ld_res = a->ld_residual; e.ld_out = a->ld_out;

@@ -72,6 +72,8 @@ struct PParams {
   float scale_log2;
   __nv_bfloat16* o;
   int64_t o_rs, o_hs;
+  const __nv_bfloat16* v;   // read again only for infinities and NaN at masked places
+  int64_t v_rs, v_hs;
   float* part_o;    // [rows][HD] normalised partial outputs
   float2* part_ml;  // [rows] (maximum in log2 units, sum)
   int* err;
@@ -189,14 +191,53 @@ __device__ __forceinline__ void scale_o(uint32_t tO, float alpha) {
   }
 }
 
-// Keys past the end of the sequence have P = 0, but 0 times whatever those rows of V hold
-// need not be 0: row `row` of a V tile in shared memory is cleared.
+// A key that a row may not see has P = 0, but 0 times an infinity or NaN in its row of V is
+// not 0.  So a V tile in shared memory is cleaned before a product that some row may not see
+// all of: rows from `valid` on (past the end of the sequence) are cleared, and with `scan`
+// infinities and NaN are taken out; returns whether any were (they are added back, in the
+// epilogue, to the rows that do see them).  128 threads, half a row each; the 16-byte pieces
+// are taken in an order that spreads the rows over the banks.
 template <int HD>
-__device__ __forceinline__ void clear_v_row(uint8_t* v_tile, int half_bytes, int row) {
-  for (int h = 0; h < HD / 64; ++h)
+__device__ __forceinline__ bool clean_v_tile(uint8_t* v_tile, int half_bytes, int t, int valid, bool scan) {
+  constexpr int PIECES = HD / 16;  // 16-byte pieces of half a row
+  const int row = t >> 1, h = t & 1;
+  bool bad = false;
+  if (row < valid && !scan) return false;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      *reinterpret_cast<uint4*>(v_tile + h * half_bytes + row * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+  for (int e = 0; e < PIECES; ++e) {
+    const int piece = ((e + row) & (PIECES - 1)) + (HD == 64 ? h * PIECES : 0);
+    uint4* at = reinterpret_cast<uint4*>(v_tile + (HD == 64 ? 0 : h * half_bytes) + row * 128 + piece * 16);
+    if (row >= valid) {
+      *at = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint4 u = *at;
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool lo = (w[i] & 0x7f80u) == 0x7f80u, hi = (w[i] & 0x7f800000u) == 0x7f800000u;
+      any |= lo | hi;
+      w[i] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
+    }
+    if (any) *at = make_uint4(w[0], w[1], w[2], w[3]);
+    bad |= any;
+  }
+  return bad;
+}
+
+// v += the infinities and NaN among 32 bf16 values.
+__device__ __forceinline__ void add_nonfinite(const __nv_bfloat16* p, float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if ((w[k] & 0x7f80u) == 0x7f80u) v[8 * i + 2 * k] += __uint_as_float(w[k] << 16);
+      if ((w[k] & 0x7f800000u) == 0x7f800000u) v[8 * i + 2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
+    }
+  }
 }
 
 // One warp's 32 finished rows as bf16, staged in shared memory (row pitch padded against
@@ -246,6 +287,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   uint64_t* v_empty = v_full + ST;  // [ST]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_empty + ST);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* bad_v = abort_flag + 1;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -266,11 +308,14 @@ __global__ void __launch_bounds__(THREADS, 2)
     key_first = part * plan.chunk[sq];
   }
   const int tok0 = (plan.tiles[sq] - 1 - tile) * p.tokens;  // later rows see more keys: first
-  int n;  // key tiles of this item
+  // key tiles of this item; `masked`: the first that some of its rows see more of than others
+  int n, masked;
   {
+    const int first = last_key(tok0, q_len, kv_len, p.causal);
     const int lk = last_key(min(tok0 + p.tokens, q_len) - 1, q_len, kv_len, p.causal);
     const int end = parts > 1 ? min(lk + 1, key_first + plan.chunk[sq]) : lk + 1;
     n = end > key_first ? (end - key_first + KTILE - 1) / KTILE : 0;
+    masked = first < lk ? max(first + 1 - key_first, 0) / KTILE : n;
   }
   auto load_k = [&](int i) {
     uint8_t* sK = smem + C::OFF_K + (i % ST) * C::TILE_BYTES;
@@ -300,6 +345,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       mbar_init(&v_empty[i], 1);
     }
     *abort_flag = 0;
+    *bad_v = 0;
     fence_barrier_init();
     griddep_wait();  // Q, K, V of the predecessor are complete
     // this thread made the barriers: its first loads need not wait for the others
@@ -406,11 +452,11 @@ __global__ void __launch_bounds__(THREADS, 2)
       ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i & 1], (i >> 1) & 1, abort_flag, p.err));
       if (!ok) break;
       tc_fence_after();
-      if (key0 + KTILE > kv_len) {
+      if (i >= masked || key0 + KTILE > kv_len) {
         ok = __all_sync(0xffffffffu, mbar_wait(&v_full[i % ST], (i / ST) & 1, abort_flag, p.err));
         if (!ok) break;
-        if (row < KTILE && row >= kv_len - key0)
-          clear_v_row<HD>(smem + C::OFF_V + (i % ST) * C::TILE_BYTES, C::HALF, row);
+        if (clean_v_tile<HD>(smem + C::OFF_V + (i % ST) * C::TILE_BYTES, C::HALF, row, kv_len - key0, i >= masked))
+          *bad_v = 1;
         fence_proxy_async_smem();
       }
       if (warp_live) {
@@ -468,6 +514,11 @@ __global__ void __launch_bounds__(THREADS, 2)
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]) * inv;
+          if (*bad_v != 0) {  // what was taken out of V, for the rows that see it
+            const __nv_bfloat16* vp = p.v + kvh * p.v_hs + e4 * 32;
+            for (int j = key_first + masked * KTILE; j <= min(lim, key_first + n * KTILE - 1); ++j)
+              add_nonfinite(vp + (kv0 + (int64_t)j) * p.v_rs, v);
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = 0.f;
@@ -758,6 +809,8 @@ ZDIT_API zdit_status zdit_prompt_attention(const zdit_prompt_attention_args* a, 
   if (!make_plan(*a, &h)) return ZDIT_ERR_SHAPE;
   if (h.q_rows > 0 && (!a->q.ptr || !a->o.ptr)) return ZDIT_ERR_INVALID_ARG;
   if (h.kv_rows > 0 && (!a->k.ptr || !a->v.ptr)) return ZDIT_ERR_INVALID_ARG;
+  if (a->o.ptr != nullptr && (a->o.ptr == a->q.ptr || a->o.ptr == a->k.ptr || a->o.ptr == a->v.ptr))
+    return ZDIT_ERR_INVALID_ARG;
   const zdit_heads* hs[4] = {&a->q, &a->k, &a->v, &a->o};
   for (int i = 0; i < 4; ++i) {
     const int n = (i == 0 || i == 3) ? a->n_heads : a->n_kv_heads;
@@ -783,6 +836,7 @@ ZDIT_API zdit_status zdit_prompt_attention(const zdit_prompt_attention_args* a, 
   const float scale = a->scale == 0.f ? 1.0f / sqrtf((float)a->head_dim) : a->scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.o = static_cast<__nv_bfloat16*>(a->o.ptr); p.o_rs = a->o.row_stride; p.o_hs = a->o.head_stride;
+  p.v = static_cast<const __nv_bfloat16*>(a->v.ptr); p.v_rs = a->v.row_stride; p.v_hs = a->v.head_stride;
   p.part_ml = static_cast<float2*>(workspace);
   p.part_o = need ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
                                              ((size_t)h.part_rows * sizeof(float2) + 255) / 256 * 256) : nullptr;

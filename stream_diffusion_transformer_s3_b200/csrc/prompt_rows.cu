@@ -142,9 +142,10 @@ __device__ __forceinline__ void store8(void* base, int64_t at, bool f32, const f
 // neighbouring heads, so a CTA reads whole stretches of a row.
 // The kernel is bound by instructions before it is bound by memory.  16381 x 40 heads of
 // 128, bf16, a quarter rotated: 87 us with 8 elements a lane and the head and token of every
-// 16 bytes found by division, 80 us with each group staying on its head (norm weights in
-// registers, addresses advancing by a row), 69 us with 16 elements a lane (two
-// tokens in flight per lane: 73 us, four: 103 us, their registers cost more threads).
+// 16 bytes found by division, 80 us with each group staying on its head (addresses advancing
+// by a row), 69 us with 16 elements a lane, 67 us with the norm weights in shared memory and
+// the registers of four CTAs per SM (two tokens in flight per lane: 73 us, four: 103 us, their
+// registers cost more threads).
 enum {
   PAIR_OWN = 0,     // interleaved: pairs inside a chunk
   PAIR_LOCAL = 1,   // halves of the whole head: element i of both chunks
@@ -215,8 +216,9 @@ struct RawChunk {
 };
 
 template <int G, int MODE, bool F32>
-__global__ void __launch_bounds__(kQkThreads, 3) qk_norm_rope_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kQkThreads, 4) qk_norm_rope_kernel(const QkParams p) {
   __shared__ float xs[MODE == PAIR_SHARED ? kQkThreads * 16 : 1];
+  __shared__ __align__(16) float ws[2][256];
   constexpr int ES = F32 ? 4 : 2;
   const int lane = threadIdx.x & (G - 1);
   const int chunks = (p.head_dim + 15) / 16;  // C
@@ -249,11 +251,13 @@ __global__ void __launch_bounds__(kQkThreads, 3) qk_norm_rope_kernel(const QkPar
   const float* sn = p.sin + t0 * p.pairs;
   griddep_wait();
   griddep_trigger();
-  float wa[8] = {}, wb[8] = {};
-  if (w != nullptr && n > 0) {
-    load8_f32(w + ea, wa);
-    if (has_b) load8_f32(w + eb, wb);
+  for (int i = threadIdx.x; i < 2 * p.head_dim; i += kQkThreads) {
+    const int k = i >= p.head_dim;
+    const float* src_w = k ? p.w_k : p.w_q;
+    if (src_w != nullptr) ws[k][i - k * p.head_dim] = src_w[i - k * p.head_dim];
   }
+  __syncthreads();
+  const float* wsm = ws[is_q ? 0 : 1];
 
   // (the same number of steps for every group: shuffles and __syncwarp need whole warps)
   constexpr int TAB = MODE == PAIR_OWN ? 4 : MODE == PAIR_SHARED ? 1 : 8;
@@ -291,11 +295,13 @@ __global__ void __launch_bounds__(kQkThreads, 3) qk_norm_rope_kernel(const QkPar
       for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       if (w != nullptr) {
         const float r = rsqrtf(fmaf(ss, p.inv_dim, p.eps));
+        float w8[8];
+        load8_f32(wsm + ea, w8);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          a[i] = a[i] * r * wa[i];
-          b[i] = b[i] * r * wb[i];
-        }
+        for (int i = 0; i < 8; ++i) a[i] = a[i] * r * w8[i];
+        if (has_b) load8_f32(wsm + eb, w8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = b[i] * r * w8[i];
       }
     }
     if constexpr (MODE == PAIR_OWN) {
@@ -447,6 +453,14 @@ ZDIT_API zdit_status zdit_qk_norm_rope(const zdit_qk_norm_rope_args* a, void* st
     if (!aligned16(hs[i]->ptr) || (a->T > 1 && hs[i]->row_stride % unit) || (n > 1 && hs[i]->head_stride % unit))
       return ZDIT_ERR_ALIGNMENT;
     if ((i & 1) && !heads_disjoint(*hs[i], a->T, n, a->head_dim)) return ZDIT_ERR_SHAPE;
+  }
+  // one buffer for input and output: in place only where every element keeps its address
+  for (int i = 0; i < 4; i += 2) {
+    const int n = i == 0 ? a->n_q : a->n_k;
+    if (n > 0 && hs[i]->ptr == hs[i + 1]->ptr &&
+        (a->in_dtype != a->out_dtype || (a->T > 1 && hs[i]->row_stride != hs[i + 1]->row_stride) ||
+         (n > 1 && hs[i]->head_stride != hs[i + 1]->head_stride)))
+      return ZDIT_ERR_INVALID_ARG;
   }
   if (!aligned16(a->w_q) || !aligned16(a->w_k) || !aligned16(a->cos) || !aligned16(a->sin)) return ZDIT_ERR_ALIGNMENT;
   if (a->T == 0) return ZDIT_OK;

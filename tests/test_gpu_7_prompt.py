@@ -298,6 +298,52 @@ def test_prompt_attention_rows_without_keys_are_zero():
 
 
 @pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("q_len,kv_len", [((150,), (150,)), ((100, 40), (130, 700)), ((3, 90), (2000, 90))])
+def test_prompt_attention_nonfinite_rows_reach_only_rows_that_see_them(q_len, kv_len, hd):
+    H, Hkv = 8, 2
+    starts = [sum(kv_len[:b]) for b in range(len(kv_len))]
+    q, k, v = rnd(1, sum(q_len), H, hd), rnd(2, sum(kv_len), Hkv, hd), rnd(3, sum(kv_len), Hkv, hd)
+    batch = Z.PromptBatch(q_len, kv_len)
+    ws = workspace(batch, H, Hkv, hd)
+    clean, o = torch.empty_like(q), torch.empty_like(q)
+    Z.zdit_prompt_attention(q, k, v, clean, batch, ws)
+    bad = [(0, kv_len[0] - 1, torch.nan, 3), (0, kv_len[0] - 3, torch.inf, hd - 1),
+           (len(kv_len) - 1, kv_len[-1] - q_len[-1] // 2, -torch.inf, 17)]
+    want = clean.double()
+    for b, j, x, d in bad:
+        v[starts[b] + j, 0, d] = x                       # key head 0: query heads 0..3
+        first = j - (kv_len[b] - q_len[b])               # first row of the sequence that sees it
+        rows = slice(sum(q_len[:b]) + max(first, 0), sum(q_len[:b + 1]))
+        want[rows, :H // Hkv, d] += x
+    Z.zdit_prompt_attention(q, k, v, o, batch, ws)
+    assert Z.zdit_device_status() == 0
+    assert torch.equal(o.isnan(), want.isnan()) and torch.equal(o.isinf(), want.isinf())
+    assert torch.equal(o[want.isinf()].double(), want[want.isinf()])
+    # what was finite is as before (a cleaned tile sums the same finite values)
+    assert torch.equal(o[want.isfinite()], clean[want.isfinite()])
+    # an infinite or NaN key changes the rows that see it and no others
+    k[starts[-1] + kv_len[-1] - 1, 1] = torch.nan
+    Z.zdit_prompt_attention(q, k, v, o, batch, ws)
+    assert o[-1, H // Hkv:].isnan().all()
+    assert torch.equal(o[:-1, H // Hkv:], clean[:-1, H // Hkv:])
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_prompt_attention_uneven_strides(hd):
+    # rows with something between and after the heads, strides that do not divide one another
+    H, Hkv, n = 6, 3, 77
+    buf = rnd(5, n, (H + 2 * Hkv) * (hd + 8) + 24)
+    cut = lambda first, heads: buf[:, first * (hd + 8):(first + heads) * (hd + 8)].view(n, heads, hd + 8)[..., :hd]
+    q, k, v = cut(0, H), cut(H, Hkv), cut(H + Hkv, Hkv)
+    o = torch.full((n, H, hd + 16), 5.0, device="cuda", dtype=torch.bfloat16)
+    batch = Z.PromptBatch([n])
+    Z.zdit_prompt_attention(q, k, v, o[..., :hd], batch, workspace(batch, H, Hkv, hd))
+    ref, bound = attention_ref(q, k, v, [n], [n], [0], True, hd ** -0.5)
+    check(o[..., :hd], ref, bound, "uneven strides")
+    assert (o[..., hd:] == 5.0).all()
+
+
+@pytest.mark.parametrize("hd", [64, 128])
 def test_prompt_attention_head_major_buffers(hd):
     run_attention((70, 133), H=6, Hkv=3, hd=hd, head_major=True)
     run_attention((1, 1), (700, 3000), (0, 700), H=6, Hkv=3, hd=hd, head_major=True)

@@ -45,8 +45,8 @@ def qk_args(**kw):
     hd = kw.get("head_dim", 128)
     nq, nk = kw.get("n_q", 4), kw.get("n_k", 2)
     a = Z.QkNormRopeArgs(T=4, n_q=4, n_k=2, head_dim=128, in_dtype=0, out_dtype=0, eps=1e-6, rotary_dim=128, layout=1)
-    a.q = a.q_out = Z.Heads(P, nq * hd, hd)
-    a.k = a.k_out = Z.Heads(P, nk * hd, hd)
+    a.q, a.q_out = Z.Heads(P, nq * hd, hd), Z.Heads(2 * P, nq * hd, hd)
+    a.k, a.k_out = Z.Heads(3 * P, nk * hd, hd), Z.Heads(4 * P, nk * hd, hd)
     a.cos = a.sin = a.w_q = a.w_k = P
     for n, v in kw.items():
         setattr(a, n, v)
@@ -63,6 +63,9 @@ def qk_args(**kw):
     (dict(q=Z.Heads(P + 8, 512, 128)), ALIGN), (dict(q=Z.Heads(P, 516, 128)), ALIGN),
     (dict(k_out=Z.Heads(P, 512, 132)), ALIGN), (dict(w_q=P + 4), ALIGN), (dict(cos=P + 4), ALIGN),
     (dict(T=1 << 33), SHAPE), (dict(T=0), 0),
+    # one buffer for input and output, but not element by element
+    (dict(q_out=Z.Heads(P, 1024, 128)), INVALID), (dict(q_out=Z.Heads(P, 512, 128), out_dtype=1), INVALID),
+    (dict(k_out=Z.Heads(3 * P, 128, 512)), INVALID),
 ])
 def test_qk_norm_rope_refusals(kw, code):
     assert Z.lib().zdit_qk_norm_rope(C.byref(qk_args(**kw)), None) == code
@@ -86,8 +89,8 @@ def pa(q_len=(3, 5), kv_len=None, kv_start=None, H=8, Hkv=2, hd=128, **kw):
         a.kv_len = i32(*kv_len)
     if kv_start is not None:
         a.kv_start = i32(*kv_start)
-    a.q = a.o = Z.Heads(P, H * hd, hd)
-    a.k = a.v = Z.Heads(P, max(Hkv, 1) * hd, hd)
+    a.q, a.o = Z.Heads(P, H * hd, hd), Z.Heads(2 * P, H * hd, hd)
+    a.k, a.v = Z.Heads(3 * P, max(Hkv, 1) * hd, hd), Z.Heads(4 * P, max(Hkv, 1) * hd, hd)
     for n, v in kw.items():
         setattr(a, n, v)
     return a
@@ -104,9 +107,10 @@ def attn(a, ws=None, n=0):
     (dict(scale=-1.0), INVALID), (dict(scale=math.inf), INVALID), (dict(scale=math.nan), INVALID),
     (dict(q=Z.Heads(None, 1024, 128)), INVALID), (dict(v=Z.Heads(None, 256, 128)), INVALID),
     (dict(q=Z.Heads(P, 64, 128)), SHAPE), (dict(k=Z.Heads(P, 256, 64)), SHAPE),
-    (dict(k=Z.Heads(P, 1 << 39, 128)), SHAPE), (dict(o=Z.Heads(P, 512, 128)), SHAPE),
+    (dict(k=Z.Heads(P, 1 << 39, 128)), SHAPE), (dict(o=Z.Heads(2 * P, 512, 128)), SHAPE),
     (dict(q=Z.Heads(P + 8, 1024, 128)), ALIGN), (dict(k=Z.Heads(P, 260, 128)), ALIGN),
-    (dict(o=Z.Heads(P, 1028, 128)), ALIGN), (dict(q_len=(0, 0)), 0),
+    (dict(o=Z.Heads(2 * P, 1028, 128)), ALIGN), (dict(q_len=(0, 0)), 0),
+    (dict(o=Z.Heads(P, 1024, 128)), INVALID), (dict(o=Z.Heads(4 * P, 1024, 128)), INVALID),
 ])
 def test_prompt_attention_refusals(a, code):
     kw = dict(a)
@@ -143,7 +147,7 @@ def test_prompt_attention_workspace():
 
 # ------------------------------------------------------------------ linear
 def lin(**kw):
-    a = Z.LinearArgs(M=4, N=8, K=16, a=P, lda=16, w=P, ldw=16, out=P, ld_out=8)
+    a = Z.LinearArgs(M=4, N=8, K=16, a=P, lda=16, w=2 * P, ldw=16, out=3 * P, ld_out=8)
     for n, v in kw.items():
         setattr(a, n, v)
     return Z.lib().zdit_linear(C.byref(a), None)
@@ -155,8 +159,10 @@ def lin(**kw):
     (dict(out=None), INVALID), (dict(N=0), SHAPE), (dict(K=0), SHAPE), (dict(N=9), SHAPE), (dict(lda=8), SHAPE),
     (dict(ldw=8), SHAPE), (dict(residual=P, ld_residual=7), SHAPE), (dict(M=(1 << 30) + 1), SHAPE),
     (dict(lda=20), ALIGN), (dict(ldw=20), ALIGN), (dict(a=P + 8), ALIGN), (dict(w=P + 2), ALIGN),
-    (dict(bias=P + 2), ALIGN), (dict(out=P + 1), ALIGN), (dict(out=P + 2, out_dtype=1), ALIGN),
+    (dict(bias=P + 2), ALIGN), (dict(out=3 * P + 1), ALIGN), (dict(out=3 * P + 2, out_dtype=1), ALIGN),
     (dict(residual=P + 2, ld_residual=8, residual_dtype=1), ALIGN), (dict(M=0), 0), (dict(M=0, a=None, out=None), 0),
+    (dict(out=P), INVALID), (dict(out=2 * P), INVALID),
+    (dict(residual=3 * P, ld_residual=8, residual_dtype=1), INVALID), (dict(residual=3 * P, ld_residual=16), INVALID),
 ])
 def test_linear_refusals(kw, code):
     assert lin(**kw) == code
