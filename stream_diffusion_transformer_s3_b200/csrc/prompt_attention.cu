@@ -195,49 +195,38 @@ __device__ __forceinline__ void scale_o(uint32_t tO, float alpha) {
 // not 0.  So a V tile in shared memory is cleaned before a product that some row may not see
 // all of: rows from `valid` on (past the end of the sequence) are cleared, and with `scan`
 // infinities and NaN are taken out; returns whether any were (they are added back, in the
-// epilogue, to the rows that do see them).  128 threads, half a row each; the 16-byte pieces
-// are taken in an order that spreads the rows over the banks.
+// epilogue, to the rows that do see them).  Looking through a masked tile costs 128 clocks of
+// shared-memory bandwidth, 5% on a batch of short prompts; to look at the outputs instead, and
+// do an item with a NaN again, measured the same.  Thread t < 128 takes half a row (or every other
+// half of its pieces); the order of the 16-byte pieces spreads eight rows over all banks.
 template <int HD>
 __device__ __forceinline__ bool clean_v_tile(uint8_t* v_tile, int half_bytes, int t, int valid, bool scan) {
   constexpr int PIECES = HD / 16;  // 16-byte pieces of half a row
-  const int row = t >> 1, h = t & 1;
-  bool bad = false;
-  if (row < valid && !scan) return false;
+  const int row = t & 63, h = t >> 6;
+  uint8_t* base = v_tile + (HD == 64 ? 0 : h * half_bytes) + row * 128;
+  auto at = [&](int e) { return base + ((e + row + (HD == 64 ? h * PIECES : 0)) & 7) * 16; };
+  if (row >= valid) {
+#pragma unroll
+    for (int e = 0; e < PIECES; ++e) *reinterpret_cast<uint4*>(at(e)) = make_uint4(0, 0, 0, 0);
+    return false;
+  }
+  if (!scan) return false;
+  // adding one unit of the exponent's last place carries into the sign bit exactly where the
+  // exponent is all ones
+  uint32_t found = 0;
 #pragma unroll
   for (int e = 0; e < PIECES; ++e) {
-    const int piece = ((e + row) & (PIECES - 1)) + (HD == 64 ? h * PIECES : 0);
-    uint4* at = reinterpret_cast<uint4*>(v_tile + (HD == 64 ? 0 : h * half_bytes) + row * 128 + piece * 16);
-    if (row >= valid) {
-      *at = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    const uint4 u = *at;
-    uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool lo = (w[i] & 0x7f80u) == 0x7f80u, hi = (w[i] & 0x7f800000u) == 0x7f800000u;
-      any |= lo | hi;
-      w[i] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
-    }
-    if (any) *at = make_uint4(w[0], w[1], w[2], w[3]);
-    bad |= any;
+    const uint4 u = *reinterpret_cast<const uint4*>(at(e));
+    found |= ((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
+             ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u);
   }
-  return bad;
-}
-
-// v += the infinities and NaN among 32 bf16 values.
-__device__ __forceinline__ void add_nonfinite(const __nv_bfloat16* p, float (&v)[32]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 u = reinterpret_cast<const uint4*>(p)[i];
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if ((w[k] & 0x7f80u) == 0x7f80u) v[8 * i + 2 * k] += __uint_as_float(w[k] << 16);
-      if ((w[k] & 0x7f800000u) == 0x7f800000u) v[8 * i + 2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
+  if ((found & 0x80008000u) == 0) return false;
+  for (int e = 0; e < PIECES; ++e)
+    for (int k = 0; k < 8; ++k) {
+      uint16_t* x = reinterpret_cast<uint16_t*>(at(e)) + k;
+      if ((*x & 0x7f80u) == 0x7f80u) *x = 0;
     }
-  }
+  return true;
 }
 
 // One warp's 32 finished rows as bf16, staged in shared memory (row pitch padded against
@@ -285,7 +274,8 @@ __global__ void __launch_bounds__(THREADS, 2)
   uint64_t* k_empty = k_full + ST;  // [ST]
   uint64_t* v_full = k_empty + ST;  // [ST]
   uint64_t* v_empty = v_full + ST;  // [ST]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_empty + ST);
+  uint64_t* v_clean = v_empty + ST; // [ST] one phase per cleaned tile of the stage
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_clean + ST);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* bad_v = abort_flag + 1;
 
@@ -308,14 +298,16 @@ __global__ void __launch_bounds__(THREADS, 2)
     key_first = part * plan.chunk[sq];
   }
   const int tok0 = (plan.tiles[sq] - 1 - tile) * p.tokens;  // later rows see more keys: first
-  // key tiles of this item; `masked`: the first that some of its rows see more of than others
-  int n, masked;
+  // key tiles of this item; the first that some of its rows see more of than others; the first
+  // whose V rows need cleaning (those, and the one that the sequence ends in)
+  int n, masked, clean_from;
   {
     const int first = last_key(tok0, q_len, kv_len, p.causal);
     const int lk = last_key(min(tok0 + p.tokens, q_len) - 1, q_len, kv_len, p.causal);
     const int end = parts > 1 ? min(lk + 1, key_first + plan.chunk[sq]) : lk + 1;
     n = end > key_first ? (end - key_first + KTILE - 1) / KTILE : 0;
     masked = first < lk ? max(first + 1 - key_first, 0) / KTILE : n;
+    clean_from = min(masked, key_first + n * KTILE > kv_len ? n - 1 : n);
   }
   auto load_k = [&](int i) {
     uint8_t* sK = smem + C::OFF_K + (i % ST) * C::TILE_BYTES;
@@ -343,6 +335,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
+      mbar_init(&v_clean[i], 2);
     }
     *abort_flag = 0;
     *bad_v = 0;
@@ -365,32 +358,49 @@ __global__ void __launch_bounds__(THREADS, 2)
   griddep_wait();     // (every thread: the outputs and the workspace are free)
   griddep_trigger();  // every CTA has started: the successor may launch
 
-  if (warp == WARP_QK) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ Q and K
-      int issued = min(n, ST);
-      for (; issued < n; ++issued) {
-        if (!mbar_wait(&k_empty[issued % ST], ((issued / ST) & 1) ^ 1, abort_flag, p.err)) break;
-        load_k(issued);
+  if (warp == WARP_QK || warp == WARP_V) {
+    // ------------------------------------------------------------ K (and Q above), V
+    // One lane loads tile i + ST when tile i is no longer needed: K when S_i is done, V when its
+    // PV product is.  Both warps clean V tiles, half of the rows each, while the softmax works.
+    // (Neither can clean tile i + ST before the MMA thread has taken tile i: that V is loaded
+    // after PV_i.  So a stage's v_clean stays within one phase of the waiting thread.)
+    const bool is_k = warp == WARP_QK;
+    int issued = min(n, ST);
+    bool ok = true;
+    auto load_next = [&](int i) {
+      if (issued >= n) return true;
+      bool go = true;
+      if (lane == 0) {
+        go = mbar_wait(is_k ? &k_empty[i % ST] : &v_empty[i % ST], (i / ST) & 1, abort_flag, p.err);
+        if (go && is_k) load_k(issued);
+        if (go && !is_k) load_v(issued);
       }
-      if (*abort_flag && n > 0) {  // let copies in flight land before shared memory is released
-        int dummy = 0;
-        mbar_wait(q_full, 0, &dummy);
-        for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(&k_full[i % ST], (i / ST) & 1, &dummy);
+      go = __all_sync(0xffffffffu, go);
+      if (go) ++issued;
+      return go;
+    };
+    for (int i = 0; ok && i < n; ++i) {
+      if (is_k && !(ok = load_next(i))) break;
+      if (i >= clean_from) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&v_full[i % ST], (i / ST) & 1, abort_flag, p.err));
+        if (!ok) break;
+        uint8_t* sV = smem + C::OFF_V + (i % ST) * C::TILE_BYTES;
+        const int valid = kv_len - key_first - i * KTILE, t = (is_k ? 0 : 64) + lane;
+        const bool bad0 = clean_v_tile<HD>(sV, C::HALF, t, valid, i >= masked);
+        const bool bad1 = clean_v_tile<HD>(sV, C::HALF, t + 32, valid, i >= masked);
+        if (bad0 || bad1) *bad_v = 1;
+        // (the tensor core has to see what was written; mostly nothing was)
+        if (__any_sync(0xffffffffu, bad0 || bad1 || valid < KTILE)) fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_clean[i % ST]);
       }
+      if (!is_k) ok = load_next(i);
     }
-  } else if (warp == WARP_V) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ V
-      int issued = min(n, ST);
-      for (; issued < n; ++issued) {
-        if (!mbar_wait(&v_empty[issued % ST], ((issued / ST) & 1) ^ 1, abort_flag, p.err)) break;
-        load_v(issued);
-      }
-      if (*abort_flag) {
-        int dummy = 0;
-        for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(&v_full[i % ST], (i / ST) & 1, &dummy);
-      }
+    if (lane == 0 && *abort_flag && n > 0) {  // let copies in flight land before shared memory is released
+      int dummy = 0;
+      if (is_k) mbar_wait(q_full, 0, &dummy);
+      for (int i = max(issued - ST, 0); i < issued; ++i)
+        mbar_wait(is_k ? &k_full[i % ST] : &v_full[i % ST], (i / ST) & 1, &dummy);
     }
   } else if (warp == WARP_MMA) {
     if (lane == 0 && n > 0) {
@@ -421,6 +431,8 @@ __global__ void __launch_bounds__(THREADS, 2)
       for (int i = 0; ok && i < n; ++i) {
         if (!(ok = mbar_wait(&p_full[i & 1], (i >> 1) & 1, abort_flag, p.err))) break;
         if (!(ok = mbar_wait(&v_full[i % ST], (i / ST) & 1, abort_flag, p.err))) break;
+        if (i >= clean_from && !(ok = mbar_wait(&v_clean[i % ST], ((i - clean_from) / ST) & 1, abort_flag, p.err)))
+          break;
         tc_fence_after();
         const uint64_t vb = dv + (i % ST) * kTileDesc;
         const uint32_t pa = tmem + (i & 1) * KTILE;
@@ -452,13 +464,6 @@ __global__ void __launch_bounds__(THREADS, 2)
       ok = __all_sync(0xffffffffu, mbar_wait(&s_full[i & 1], (i >> 1) & 1, abort_flag, p.err));
       if (!ok) break;
       tc_fence_after();
-      if (i >= masked || key0 + KTILE > kv_len) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&v_full[i % ST], (i / ST) & 1, abort_flag, p.err));
-        if (!ok) break;
-        if (clean_v_tile<HD>(smem + C::OFF_V + (i % ST) * C::TILE_BYTES, C::HALF, row, kv_len - key0, i >= masked))
-          *bad_v = 1;
-        fence_proxy_async_smem();
-      }
       if (warp_live) {
         const uint32_t tS = tmem + lane_off + (i & 1) * KTILE;
         float s[KTILE];
@@ -514,11 +519,6 @@ __global__ void __launch_bounds__(THREADS, 2)
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]) * inv;
-          if (*bad_v != 0) {  // what was taken out of V, for the rows that see it
-            const __nv_bfloat16* vp = p.v + kvh * p.v_hs + e4 * 32;
-            for (int j = key_first + masked * KTILE; j <= min(lim, key_first + n * KTILE - 1); ++j)
-              add_nonfinite(vp + (kv0 + (int64_t)j) * p.v_rs, v);
-          }
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = 0.f;
@@ -541,6 +541,24 @@ __global__ void __launch_bounds__(THREADS, 2)
         // every product is done: Q and the rings are idle
         store_rows<HD>(smem + warp * 32 * (2 * HD + 16), lane,
                        live ? (q0 + (int64_t)tok) * p.o_rs + head * p.o_hs : -1, p.o, take);
+      }
+      if (*bad_v != 0) {
+        // infinities and NaN were taken out of V: added to the stored rows that see them
+        __syncwarp();
+        for (int j = key_first + masked * KTILE; live && j <= min(lim, key_first + n * KTILE - 1); ++j) {
+          const __nv_bfloat16* vp = p.v + (kv0 + (int64_t)j) * p.v_rs + kvh * p.v_hs;
+          for (int e = 0; e < HD; ++e) {
+            const float x = __bfloat162float(vp[e]);
+            if (isfinite(x)) continue;
+            if (parts > 1) {
+              const int64_t at = (int64_t)plan.part0[sq] + ((int64_t)part * q_len + tok) * (p.n_kv * p.group) + head;
+              p.part_o[at * HD + e] += x;
+            } else {
+              __nv_bfloat16* op = p.o + (q0 + (int64_t)tok) * p.o_rs + head * p.o_hs + e;
+              *op = __float2bfloat16_rn(__bfloat162float(*op) + x);
+            }
+          }
+        }
       }
     }
     tc_fence_before();
