@@ -388,6 +388,8 @@ _attn_args = _packer(PromptAttentionArgs, "@i4xPPP4if4xPqqPqqPqqPqq")
 _linear_args = _packer(LinearArgs, "@qqqPqPqPi4xPqi4xPqi4x")
 
 
+# (These run on every call of kernels that take a few us, so they read each property of a
+# tensor once and format messages only on failure.)
 def _dtype_code(t, where):
     T = _th()
     dt = t.dtype
@@ -415,13 +417,14 @@ def _f32(where, name, t, *shape):
     """Address of a contiguous fp32 tensor of that shape, 0 of None."""
     if t is None:
         return 0
-    if t.dtype is not _th().float32 or t.shape != shape or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not _th().float32 or not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be a contiguous float32 {list(shape)}")
     return t.data_ptr()
 
 
 def _heads(where, name, t, shape):
-    """Heads fields of a [rows, heads, head_dim] tensor whose last axis is contiguous."""
+    """Heads fields (address, row stride, head stride) of a tensor of that [rows, heads,
+    head_dim] shape whose last axis is contiguous."""
     if len(shape) != 3 or t.shape != shape:
         raise ValueError(f"{where}: {name} has shape {list(t.shape)}, expected [rows, heads, head_dim] = {list(shape)}")
     rs, hs, es = t.stride()
@@ -449,16 +452,18 @@ def zdit_qk_norm_rope(q, k, q_out, k_out, w_q, w_k, cos, sin, rotary_dim, layout
     head_dim] and k [T, n_k, head_dim] (k and k_out may be None) into q_out, k_out (which may
     be q and k themselves)."""
     w = "zdit_qk_norm_rope"
-    T, n_q, hd = q.shape
-    hq, hqo = _heads(w, "q", q, (T, n_q, hd)), _heads(w, "q_out", q_out, (T, n_q, hd))
+    shape = q.shape
+    hq, hqo = _heads(w, "q", q, shape), _heads(w, "q_out", q_out, shape)
+    T, n_q, hd = shape
     if (k is None) != (k_out is None):
         raise ValueError(f"{w}: k and k_out go together")
     n_k, hk, hko = 0, _NO_HEADS, _NO_HEADS
     if k is not None:
-        n_k = k.shape[1]
-        if k.dtype is not q.dtype or k_out.dtype is not q_out.dtype:
-            raise ValueError(f"{w}: k must have q's type and k_out q_out's")
-        hk, hko = _heads(w, "k", k, (T, n_k, hd)), _heads(w, "k_out", k_out, (T, n_k, hd))
+        kshape = k.shape
+        if k.dtype is not q.dtype or k_out.dtype is not q_out.dtype or kshape[0] != T or kshape[2] != hd:
+            raise ValueError(f"{w}: k must have q's type, rows and head_dim, and k_out q_out's type")
+        n_k = kshape[1]
+        hk, hko = _heads(w, "k", k, kshape), _heads(w, "k_out", k_out, kshape)
     pq, pk = _f32(w, "w_q", w_q, hd), _f32(w, "w_k", w_k, hd)
     pc, ps = 0, 0
     if rotary_dim:
@@ -508,10 +513,13 @@ def zdit_prompt_attention(q, k, v, o, batch: PromptBatch, workspace=None, causal
     bf = _th().bfloat16
     if not (q.dtype is bf and k.dtype is bf and v.dtype is bf and o.dtype is bf):
         raise ValueError(f"{w}: q, k, v and o must be bfloat16")
-    (R, H, hd), (S, Hkv, _) = q.shape, k.shape
-    hq, ho = _heads(w, "q", q, (R, H, hd)), _heads(w, "o", o, (o.shape[0], H, hd))
-    hk, hv = _heads(w, "k", k, (S, Hkv, hd)), _heads(w, "v", v, (S, Hkv, hd))
-    if R < batch.q_rows or o.shape[0] < batch.q_rows or S < batch.kv_rows:
+    qs, ks, os_ = q.shape, k.shape, o.shape
+    hq, ho = _heads(w, "q", q, qs), _heads(w, "o", o, os_)
+    hk, hv = _heads(w, "k", k, ks), _heads(w, "v", v, ks)
+    (R, H, hd), (S, Hkv, khd), (Ro, Ho, ohd) = qs, ks, os_
+    if Ho != H or not hd == khd == ohd:
+        raise ValueError(f"{w}: o must have q's heads, and all the same head_dim")
+    if R < batch.q_rows or Ro < batch.q_rows or S < batch.kv_rows:
         raise ValueError(f"{w}: the batch needs {batch.q_rows} rows of q and o and {batch.kv_rows} of k and v")
     s = _launch_stream(w, stream, q, k, v, o, workspace)
     a = batch.args(H, Hkv, hd, causal, scale, hq + hk + hv + ho)
