@@ -117,20 +117,21 @@ struct QkParams {
   int in_f32, out_f32;
 };
 
-__device__ __forceinline__ void load8_f32(const float* p, float (&v)[8]) {
-  const float4* s = reinterpret_cast<const float4*>(p);
-  const float4 a = s[0], b = s[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// v = v * r * w for the 8 values of a chunk.
+__device__ __forceinline__ void scale8(float (&v)[8], float r, const float4* w, int chunks) {
+  const float4 w0 = w[0], w1 = w[chunks];
+  v[0] = v[0] * r * w0.x; v[1] = v[1] * r * w0.y; v[2] = v[2] * r * w0.z; v[3] = v[3] * r * w0.w;
+  v[4] = v[4] * r * w1.x; v[5] = v[5] * r * w1.y; v[6] = v[6] * r * w1.z; v[7] = v[7] * r * w1.w;
 }
 
-__device__ __forceinline__ void store8(void* base, int64_t at, bool f32, const float (&v)[8]) {
-  if (f32) {
-    float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+template <bool F32>
+__device__ __forceinline__ void store8(char* at, const float (&v)[8]) {
+  if constexpr (F32) {
+    float4* d = reinterpret_cast<float4*>(at);
     d[0] = make_float4(v[0], v[1], v[2], v[3]);
     d[1] = make_float4(v[4], v[5], v[6], v[7]);
   } else {
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at) =
+    *reinterpret_cast<uint4*>(at) =
         make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   }
 }
@@ -147,17 +148,18 @@ __device__ __forceinline__ void store8(void* base, int64_t at, bool f32, const f
 // the registers of four CTAs per SM (two tokens in flight per lane: 73 us, four: 103 us, their
 // registers cost more threads).
 enum {
-  PAIR_OWN = 0,     // interleaved: pairs inside a chunk
+  PAIR_OWN = 0,     // interleaved: pairs inside a chunk, tables in multiples of 4 pairs
   PAIR_LOCAL = 1,   // halves of the whole head: element i of both chunks
   PAIR_SHUFFLE = 2, // halves inside the first chunks: another lane's elements
-  PAIR_SHARED = 3   // any other split: through shared memory
+  PAIR_SHARED = 3,  // any other split: through shared memory
+  PAIR_ODD = 4      // interleaved, any number of pairs
 };
-// The rotation tables of one lane and token: 4 or 8 pairs, and (PAIR_OWN) 4 more for the
-// second chunk.
-template <int N>
-__device__ __forceinline__ void load_pairs(const float* cs, const float* sn, int i0, int pairs, bool vec, float (&c)[N],
+// The rotation tables of one lane and token: N pairs from i0; ODD: one by one, the identity
+// past the last.
+template <int N, bool ODD>
+__device__ __forceinline__ void load_pairs(const float* cs, const float* sn, int i0, int pairs, float (&c)[N],
                                            float (&s)[N]) {
-  if (vec) {
+  if constexpr (!ODD) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
       const float4 c4 = *reinterpret_cast<const float4*>(cs + i0 + i), s4 = *reinterpret_cast<const float4*>(sn + i0 + i);
@@ -174,11 +176,12 @@ __device__ __forceinline__ void load_pairs(const float* cs, const float* sn, int
   }
 }
 
+template <bool ODD>
 __device__ __forceinline__ void rotate_own(float (&v)[8], const float (&c)[4], const float (&s)[4], int i0, int pairs) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float x = v[2 * i], y = v[2 * i + 1];
-    if (i0 + i < pairs) {
+    if (!ODD || i0 + i < pairs) {
       v[2 * i] = x * c[i] - y * s[i];
       v[2 * i + 1] = x * s[i] + y * c[i];
     }
@@ -215,11 +218,14 @@ struct RawChunk {
   }
 };
 
-template <int G, int MODE, bool F32>
+template <int G, int MODE, bool F32, bool OUT_F32>
 __global__ void __launch_bounds__(kQkThreads, 4) qk_norm_rope_kernel(const QkParams p) {
   __shared__ float xs[MODE == PAIR_SHARED ? kQkThreads * 16 : 1];
-  __shared__ __align__(16) float ws[2][256];
-  constexpr int ES = F32 ? 4 : 2;
+  // norm weights: the first halves of all chunks of 8, then the second halves, so that
+  // neighbouring lanes read neighbouring 16 bytes
+  __shared__ float4 ws[2][64];
+  constexpr int ES = F32 ? 4 : 2, OES = OUT_F32 ? 4 : 2;
+  constexpr bool OWN = MODE == PAIR_OWN || MODE == PAIR_ODD;
   const int lane = threadIdx.x & (G - 1);
   const int chunks = (p.head_dim + 15) / 16;  // C
   const int ea = lane * 8, eb = (chunks + lane) * 8;
@@ -233,20 +239,18 @@ __global__ void __launch_bounds__(kQkThreads, 4) qk_norm_rope_kernel(const QkPar
   const bool is_q = h < p.n_q;
   if (!is_q) h -= p.n_q;
   const int64_t rs = is_q ? p.q_rs : p.k_rs, ors = is_q ? p.qo_rs : p.ko_rs;
-  const int oes = p.out_f32 ? 4 : 2;
   const char* src = static_cast<const char*>(is_q ? p.q : p.k) + ((is_q ? h * p.q_hs : h * p.k_hs) + t0 * rs + ea) * ES;
-  char* dst = static_cast<char*>(is_q ? p.qo : p.ko) + ((is_q ? h * p.qo_hs : h * p.ko_hs) + t0 * ors + ea) * oes;
-  const int64_t src_step = rs * ES, dst_step = ors * oes;
-  const int src_b = chunks * 8 * ES, dst_b = chunks * 8;  // second chunk: bytes, elements
+  char* dst = static_cast<char*>(is_q ? p.qo : p.ko) + ((is_q ? h * p.qo_hs : h * p.ko_hs) + t0 * ors + ea) * OES;
+  const int64_t src_step = rs * ES, dst_step = ors * OES;
+  const int src_b = chunks * 8 * ES, dst_b = chunks * 8 * OES;  // to the second chunk
   const float* w = is_q ? p.w_q : p.w_k;
   const bool norms = p.w_q != nullptr || p.w_k != nullptr;
   const int step = p.pairs / 8;  // PAIR_SHUFFLE: lanes between partners
   const bool lo = lane < step, hi = !lo && lane < 2 * step;
   const int partner = lo ? lane + step : (hi ? lane - step : lane);
-  const int i0 = MODE == PAIR_OWN ? ea / 2 : MODE == PAIR_SHUFFLE && hi ? ea - p.pairs : ea;  // first pair of chunk a
-  const bool rotates = MODE == PAIR_OWN ? i0 < p.pairs : MODE == PAIR_LOCAL ? true : (lo || hi);
-  const bool rotates_b = MODE == PAIR_OWN && has_b && eb / 2 < p.pairs;
-  const bool vec = (p.pairs & 3) == 0;
+  const int i0 = OWN ? ea / 2 : MODE == PAIR_SHUFFLE && hi ? ea - p.pairs : ea;  // first pair of chunk a
+  const bool rotates = OWN ? i0 < p.pairs : MODE == PAIR_LOCAL ? true : (lo || hi);
+  const bool rotates_b = OWN && has_b && eb / 2 < p.pairs;
   const float* cs = p.cos + t0 * p.pairs;
   const float* sn = p.sin + t0 * p.pairs;
   griddep_wait();
@@ -254,23 +258,24 @@ __global__ void __launch_bounds__(kQkThreads, 4) qk_norm_rope_kernel(const QkPar
   for (int i = threadIdx.x; i < 2 * p.head_dim; i += kQkThreads) {
     const int k = i >= p.head_dim;
     const float* src_w = k ? p.w_k : p.w_q;
-    if (src_w != nullptr) ws[k][i - k * p.head_dim] = src_w[i - k * p.head_dim];
+    const int e = i - k * p.head_dim;
+    if (src_w != nullptr) reinterpret_cast<float*>(&ws[k][(e >> 2 & 1) * (p.head_dim / 8) + e / 8])[e & 3] = src_w[e];
   }
   __syncthreads();
-  const float* wsm = ws[is_q ? 0 : 1];
+  const float4* wsm = ws[is_q ? 0 : 1];
 
   // (the same number of steps for every group: shuffles and __syncwarp need whole warps)
-  constexpr int TAB = MODE == PAIR_OWN ? 4 : MODE == PAIR_SHARED ? 1 : 8;
-  constexpr int TAB_B = MODE == PAIR_OWN ? 4 : 1;
+  constexpr int TAB = OWN ? 4 : MODE == PAIR_SHARED ? 1 : 8;
+  constexpr int TAB_B = OWN ? 4 : 1;
   RawChunk<F32> ra, rb;
   float c[TAB], s[TAB], cb[TAB_B], sb[TAB_B];
   auto request = [&](bool live) {  // the head and table rows that src, cs and sn point at
     ra.load(src, live);
     rb.load(src + src_b, live && has_b);
     if constexpr (MODE != PAIR_SHARED) {
-      if (live && rotates) load_pairs<TAB>(cs, sn, i0, p.pairs, vec, c, s);
-      if constexpr (MODE == PAIR_OWN)
-        if (live && rotates_b) load_pairs<4>(cs, sn, eb / 2, p.pairs, vec, cb, sb);
+      if (live && rotates) load_pairs<TAB, MODE == PAIR_ODD>(cs, sn, i0, p.pairs, c, s);
+      if constexpr (OWN)
+        if (live && rotates_b) load_pairs<4, MODE == PAIR_ODD>(cs, sn, eb / 2, p.pairs, cb, sb);
     }
   };
   for (int k = 0; k < p.tokens; ++k) {
@@ -295,18 +300,13 @@ __global__ void __launch_bounds__(kQkThreads, 4) qk_norm_rope_kernel(const QkPar
       for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       if (w != nullptr) {
         const float r = rsqrtf(fmaf(ss, p.inv_dim, p.eps));
-        float w8[8];
-        load8_f32(wsm + ea, w8);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = a[i] * r * w8[i];
-        if (has_b) load8_f32(wsm + eb, w8);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = b[i] * r * w8[i];
+        scale8(a, r, wsm + (n > 0 ? lane : 0), p.head_dim / 8);
+        scale8(b, r, wsm + (has_b ? chunks + lane : 0), p.head_dim / 8);
       }
     }
-    if constexpr (MODE == PAIR_OWN) {
-      if (rotates) rotate_own(a, c, s, i0, p.pairs);
-      if (rotates_b) rotate_own(b, cb, sb, eb / 2, p.pairs);
+    if constexpr (OWN) {
+      if (rotates) rotate_own<MODE == PAIR_ODD>(a, c, s, i0, p.pairs);
+      if (rotates_b) rotate_own<MODE == PAIR_ODD>(b, cb, sb, eb / 2, p.pairs);
     } else if constexpr (MODE == PAIR_LOCAL) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(kQkThreads, 4) qk_norm_rope_kernel(const QkPar
       }
     }
     if (live) {
-      store8(dst, 0, p.out_f32, a);
-      if (has_b) store8(dst, dst_b, p.out_f32, b);
+      store8<OUT_F32>(dst, a);
+      if (has_b) store8<OUT_F32>(dst + dst_b, b);
     }
     dst += dst_step;
   }
@@ -357,9 +357,12 @@ __global__ void __launch_bounds__(kQkThreads, 4) qk_norm_rope_kernel(const QkPar
 template <int G, int MODE>
 cudaError_t launch_qk_mode(const QkParams& p, cudaStream_t s) {
   const int64_t groups = (p.T + p.tokens - 1) / p.tokens * (p.n_q + p.n_k), per = kQkThreads / G;
-  const dim3 grid((unsigned)((groups + per - 1) / per));
-  return p.in_f32 ? launch_dependent(qk_norm_rope_kernel<G, MODE, true>, grid, dim3(kQkThreads), 0, s, p)
-                  : launch_dependent(qk_norm_rope_kernel<G, MODE, false>, grid, dim3(kQkThreads), 0, s, p);
+  const dim3 grid((unsigned)((groups + per - 1) / per)), block(kQkThreads);
+  if (p.in_f32)
+    return p.out_f32 ? launch_dependent(qk_norm_rope_kernel<G, MODE, true, true>, grid, block, 0, s, p)
+                     : launch_dependent(qk_norm_rope_kernel<G, MODE, true, false>, grid, block, 0, s, p);
+  return p.out_f32 ? launch_dependent(qk_norm_rope_kernel<G, MODE, false, true>, grid, block, 0, s, p)
+                   : launch_dependent(qk_norm_rope_kernel<G, MODE, false, false>, grid, block, 0, s, p);
 }
 
 template <int G>
@@ -368,6 +371,7 @@ cudaError_t launch_qk_group(const QkParams& p, int mode, cudaStream_t s) {
     case PAIR_OWN: return launch_qk_mode<G, PAIR_OWN>(p, s);
     case PAIR_LOCAL: return launch_qk_mode<G, PAIR_LOCAL>(p, s);
     case PAIR_SHUFFLE: return launch_qk_mode<G, PAIR_SHUFFLE>(p, s);
+    case PAIR_ODD: return launch_qk_mode<G, PAIR_ODD>(p, s);
     default: return launch_qk_mode<G, PAIR_SHARED>(p, s);
   }
 }
@@ -479,7 +483,7 @@ ZDIT_API zdit_status zdit_qk_norm_rope(const zdit_qk_norm_rope_args* a, void* st
   p.w_q = a->w_q; p.w_k = a->w_k; p.cos = a->cos; p.sin = a->sin; p.eps = a->eps; p.inv_dim = 1.0f / a->head_dim;
   p.in_f32 = a->in_dtype == ZDIT_T_F32; p.out_f32 = a->out_dtype == ZDIT_T_F32;
   const int half = (a->head_dim + 15) / 16 * 8;  // first element of the second chunks
-  const int mode = a->layout == ZDIT_ROPE_INTERLEAVED          ? PAIR_OWN
+  const int mode = a->layout == ZDIT_ROPE_INTERLEAVED          ? (p.pairs % 4 == 0 ? PAIR_OWN : PAIR_ODD)
                    : p.pairs == half && a->rotary_dim == a->head_dim ? PAIR_LOCAL
                    : p.pairs % 8 == 0 && a->rotary_dim <= half ? PAIR_SHUFFLE
                                                                : PAIR_SHARED;
