@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
-      mbar_init(&v_clean[i], 2);
+      mbar_init(&v_clean[i], 1);
     }
     *abort_flag = 0;
     *bad_v = 0;
@@ -358,49 +358,58 @@ __global__ void __launch_bounds__(THREADS, 2)
   griddep_wait();     // (every thread: the outputs and the workspace are free)
   griddep_trigger();  // every CTA has started: the successor may launch
 
-  if (warp == WARP_QK || warp == WARP_V) {
-    // ------------------------------------------------------------ K (and Q above), V
-    // One lane loads tile i + ST when tile i is no longer needed: K when S_i is done, V when its
-    // PV product is.  Both warps clean V tiles, half of the rows each, while the softmax works.
-    // (Neither can clean tile i + ST before the MMA thread has taken tile i: that V is loaded
-    // after PV_i.  So a stage's v_clean stays within one phase of the waiting thread.)
-    const bool is_k = warp == WARP_QK;
+  if (warp == WARP_QK) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ K (and Q above)
+      int issued = min(n, ST);
+      for (; issued < n; ++issued) {
+        if (!mbar_wait(&k_empty[issued % ST], ((issued / ST) & 1) ^ 1, abort_flag, p.err)) break;
+        load_k(issued);
+      }
+      if (*abort_flag && n > 0) {  // let copies in flight land before shared memory is released
+        int dummy = 0;
+        mbar_wait(q_full, 0, &dummy);
+        for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(&k_full[i % ST], (i / ST) & 1, &dummy);
+      }
+    }
+  } else if (warp == WARP_V) {
+    // ------------------------------------------------------------ V
+    // The warp cleans tile i while the softmax works on it, then one lane loads tile i + ST when
+    // the PV product of tile i is done.  A barrier only tells the phase before the current one
+    // from the current one, so whoever waits for a tile of a stage must not be a round ahead of
+    // it: this warp has loaded the tile that it waits for, and it cannot clean the next one of
+    // the stage before the MMA thread has taken this one.  (No other warp can help: it could be
+    // ahead of the loads.)
     int issued = min(n, ST);
     bool ok = true;
-    auto load_next = [&](int i) {
-      if (issued >= n) return true;
-      bool go = true;
-      if (lane == 0) {
-        go = mbar_wait(is_k ? &k_empty[i % ST] : &v_empty[i % ST], (i / ST) & 1, abort_flag, p.err);
-        if (go && is_k) load_k(issued);
-        if (go && !is_k) load_v(issued);
-      }
-      go = __all_sync(0xffffffffu, go);
-      if (go) ++issued;
-      return go;
-    };
-    for (int i = 0; ok && i < n; ++i) {
-      if (is_k && !(ok = load_next(i))) break;
+    for (int i = 0; i < n; ++i) {
       if (i >= clean_from) {
         ok = __all_sync(0xffffffffu, mbar_wait(&v_full[i % ST], (i / ST) & 1, abort_flag, p.err));
         if (!ok) break;
         uint8_t* sV = smem + C::OFF_V + (i % ST) * C::TILE_BYTES;
-        const int valid = kv_len - key_first - i * KTILE, t = (is_k ? 0 : 64) + lane;
-        const bool bad0 = clean_v_tile<HD>(sV, C::HALF, t, valid, i >= masked);
-        const bool bad1 = clean_v_tile<HD>(sV, C::HALF, t + 32, valid, i >= masked);
-        if (bad0 || bad1) *bad_v = 1;
+        const int valid = kv_len - key_first - i * KTILE;
+        bool bad = false;
+#pragma unroll
+        for (int t = 0; t < 128; t += 32) bad |= clean_v_tile<HD>(sV, C::HALF, t + lane, valid, i >= masked);
+        if (bad) *bad_v = 1;
         // (the tensor core has to see what was written; mostly nothing was)
-        if (__any_sync(0xffffffffu, bad0 || bad1 || valid < KTILE)) fence_proxy_async_smem();
+        if (__any_sync(0xffffffffu, bad || valid < KTILE)) fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_clean[i % ST]);
       }
-      if (!is_k) ok = load_next(i);
+      if (issued < n) {  // tile i + ST
+        if (lane == 0) {
+          ok = mbar_wait(&v_empty[i % ST], (i / ST) & 1, abort_flag, p.err);
+          if (ok) load_v(issued);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++issued;
+      }
     }
-    if (lane == 0 && *abort_flag && n > 0) {  // let copies in flight land before shared memory is released
+    if (lane == 0 && *abort_flag) {
       int dummy = 0;
-      if (is_k) mbar_wait(q_full, 0, &dummy);
-      for (int i = max(issued - ST, 0); i < issued; ++i)
-        mbar_wait(is_k ? &k_full[i % ST] : &v_full[i % ST], (i / ST) & 1, &dummy);
+      for (int i = max(issued - ST, 0); i < issued; ++i) mbar_wait(&v_full[i % ST], (i / ST) & 1, &dummy);
     }
   } else if (warp == WARP_MMA) {
     if (lane == 0 && n > 0) {

@@ -414,6 +414,37 @@ def test_prompt_attention_is_deterministic_and_replays():
     check(o3[:4], ref, bound, "replay on new data")
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("q_len,kv_len", [
+    ((1,) * 8, (8191, 2501, 6000, 3333, 4097, 5555, 7001, 2999)),
+    (tuple(range(30, 400, 17)), None),
+    ((333, 500, 1), (4001, 2999, 8001)),
+])
+def test_prompt_attention_under_load_back_to_back(q_len, kv_len, hd):
+    # enough work to keep every SM and the memory busy, so that the warps of a CTA drift apart;
+    # sequences that end inside a key tile; calls queued behind one another on two sets of buffers
+    H, Hkv = 32, 8
+    lens = q_len if kv_len is None else kv_len
+    cap = (max(lens) + 63) // 64 * 64
+    starts = [b * cap for b in range(len(lens))] if kv_len else [sum(lens[:b]) for b in range(len(lens))]
+    rows = starts[-1] + (cap if kv_len else lens[-1])
+    batch = Z.PromptBatch(q_len, kv_len, starts)
+    sets = []
+    for i in range(2):
+        q, k, v = rnd(10 + i, sum(q_len), H, hd), rnd(20 + i, rows, Hkv, hd), rnd(30 + i, rows, Hkv, hd)
+        sets.append((q, k, v, workspace(batch, H, Hkv, hd)))
+    torch.cuda.synchronize()
+    outs = [[torch.empty_like(sets[i][0]) for _ in range(6)] for i in range(2)]
+    for r in range(6):
+        for i, (q, k, v, ws) in enumerate(sets):
+            Z.zdit_prompt_attention(q, k, v, outs[i][r], batch, ws)
+    for i, (q, k, v, ws) in enumerate(sets):
+        ref, bound = attention_ref(q, k, v, q_len, lens, starts, True, hd ** -0.5)
+        for r in range(6):
+            check(outs[i][r], ref, bound, f"set {i} call {r}")
+            assert torch.equal(outs[i][r], outs[i][0])
+
+
 def test_prompt_attention_far_row_offsets():
     # key rows whose offsets pass 2^31 elements: 33 M rows of one head, the last ones used
     rows, hd = (1 << 25) + 1000, 64
