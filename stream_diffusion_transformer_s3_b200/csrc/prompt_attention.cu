@@ -389,7 +389,8 @@ __global__ void __launch_bounds__(THREADS, 2)
         uint8_t* sV = smem + C::OFF_V + (i % ST) * C::TILE_BYTES;
         const int valid = kv_len - key_first - i * KTILE;
         bool bad = false;
-#pragma unroll
+        // (as a loop: its four turns unrolled made the 24 captions' call 38.4 us instead of 34.2)
+#pragma unroll 1
         for (int t = 0; t < 128; t += 32) bad |= clean_v_tile<HD>(sV, C::HALF, t + lane, valid, i >= masked);
         if (bad) *bad_v = 1;
         // (the tensor core has to see what was written; mostly nothing was)
