@@ -369,7 +369,10 @@ ZDIT_API zdit_status zdit_gemm_bf16(const void* A, const void* B, float* C, int6
  * rotation, attention that is causal, has fewer key heads than query heads and runs over
  * prompts of different lengths packed one after the other, and projections that add
  * bias, activation and residual.  The four calls below are forward only, like the rest
- * of the library. */
+ * of the library.  They return once their work is queued on the stream, need the tensors'
+ * device to be the current one, and may be captured into graphs; zdit_profile_begin
+ * records them under the kernel kinds that they resemble (rope_table, norm_modulate,
+ * attention, gemm_other). */
 
 /* Element types of the buffers whose type a call leaves open. */
 enum { ZDIT_T_BF16 = 0, ZDIT_T_F32 = 1 };
@@ -499,7 +502,7 @@ ZDIT_API zdit_status zdit_prompt_attention(const zdit_prompt_attention_args* a, 
  *   act        ZDIT_ACT_* (GELU: y Phi(y); GELU_TANH: its tanh form)
  *   residual   residual_dtype [M, N], row stride ld_residual, or NULL; may be out itself
  *              (pointer, stride and type alike), otherwise does not overlap it
- *   out        out_dtype [M, N], row stride ld_out
+ *   out        out_dtype [M, N], row stride ld_out; does not overlap a, w or bias
  * Any M >= 0, N, K >= 1.  a and w 16-byte aligned with strides that are multiples of 8
  * elements (K need not be); bias, residual and out aligned to their element.  Columns past
  * K and rows past M or N are never used.  Errors: ZDIT_ERR_INVALID_ARG, ZDIT_ERR_SHAPE,

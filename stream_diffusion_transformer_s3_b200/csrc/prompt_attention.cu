@@ -20,8 +20,10 @@
 // Per 128 x 64 unit the tensor core works 8 x 48 + 4 x 64 = 640 clocks (S reads both operands
 // from shared memory, 48 clocks a step instead of 32), the exponentials take 512, and shared
 // memory moves 32 KB of K and V in and 64 KB of operands out, 768: long prompts are bound
-// there (16384 tokens, 32 heads on 8: 1.85 ms, 1190 TFLOP/s); a short item is mostly set-up,
-// load latency and output (one key tile 4.8 us, 0.65 us for each further one).
+// there (16384 tokens, 32 heads on 8: 2.0 to 2.1 ms, 1.05 to 1.1 PFLOP/s; under the power cap
+// 2.15 to 2.2 ms); a short item is mostly set-up, load latency and output (one key tile 4.3 us,
+// each further one 0.7 us), two of them at a time on an SM (24 captions of 8 to 512 tokens, 32
+// heads on 8: 34 us, 2.5 times the floor of their products and bytes).
 // Measured and not kept: two query tiles and 128-key tiles per CTA, one CTA per SM (half the K
 // and V traffic, but it waits for its own softmax: 1.0 to 1.6 times slower from 300 to 16384
 // tokens with 8 key heads); a persistent kernel that loads the next item while it finishes the
@@ -195,10 +197,11 @@ __device__ __forceinline__ void scale_o(uint32_t tO, float alpha) {
 // not 0.  So a V tile in shared memory is cleaned before a product that some row may not see
 // all of: rows from `valid` on (past the end of the sequence) are cleared, and with `scan`
 // infinities and NaN are taken out; returns whether any were (they are added back, in the
-// epilogue, to the rows that do see them).  Looking through a masked tile costs 128 clocks of
-// shared-memory bandwidth, 5% on a batch of short prompts; to look at the outputs instead, and
-// do an item with a NaN again, measured the same.  Thread t < 128 takes half a row (or every other
-// half of its pieces); the order of the 16-byte pieces spreads eight rows over all banks.
+// epilogue, to the rows that do see them).  It costs 5% on a batch of short prompts (32.6 us
+// without, 34.3 with, 24 captions of 8 to 512 tokens) and nothing where few tiles are masked; to
+// look at the outputs instead, and do an item with a NaN again, measured the same.  Half row t <
+// 128 (at head_dim 64 every other half of its pieces); the order of the 16-byte pieces spreads
+// eight rows over all banks.
 template <int HD>
 __device__ __forceinline__ bool clean_v_tile(uint8_t* v_tile, int half_bytes, int t, int valid, bool scan) {
   constexpr int PIECES = HD / 16;  // 16-byte pieces of half a row
@@ -537,13 +540,27 @@ __global__ void __launch_bounds__(THREADS, 2)
       if (parts > 1) {
         const int64_t at = (int64_t)plan.part0[sq] + ((int64_t)part * q_len + tok) * (p.n_kv * p.group) + head;
         if (live) p.part_ml[at] = make_float2(m_ref, l_sum);
+        // through shared memory (every product is done: Q and the rings are idle), so that a
+        // store instruction writes four whole lines instead of 16 bytes of 32 (100 tokens, 32 heads
+        // on 8, 2000 keys: 17.3 -> 15.0 us; single tokens, 4 rows of a tile: 36.9 -> 37.2 us)
+        constexpr int PITCH = 128 + 16;
+        uint8_t* stage = smem + warp * 32 * PITCH;
+        const long long off = live ? at * HD : -1;
+        const int rows = __popc(__ballot_sync(0xffffffffu, live));  // the live rows come first
         for (int e4 = 0; e4 < HD / 32; ++e4) {
           float v[32];
           take(e4, v);
-          if (live) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + at * HD + e4 * 32);
+          float4* dst = reinterpret_cast<float4*>(stage + lane * PITCH);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int it = 0; it < 8; ++it) {
+            if (it * 4 >= rows) break;
+            const int r = it * 4 + lane / 8;
+            const long long ro = __shfl_sync(0xffffffffu, off, r);
+            const float4 f = *reinterpret_cast<const float4*>(stage + r * PITCH + (lane % 8) * 16);
+            if (ro >= 0) *reinterpret_cast<float4*>(p.part_o + ro + e4 * 32 + (lane % 8) * 4) = f;
           }
           __syncwarp();
         }
@@ -586,7 +603,8 @@ __global__ void __launch_bounds__(THREADS, 2)
 // dependent loads, so everything that does not come from the parts is found before the wait,
 // and the partial rows are requested together with their maxima.  Four warps a row while the
 // rows are few (32 parts of 4 rows: 8 us with one warp, 2 us with four), one when they fill the
-// GPU by themselves (2664 rows of 10 parts: JOIN_ONE).
+// GPU by themselves (2664 rows of 10 parts: 8.7 us with four, 5.4 us with one; two warps a row,
+// or 5 or 16 parts requested at a time, are within 10% of that or slower).
 constexpr int kJoinThreads = 128;
 template <int HD, int WPR>
 __global__ void __launch_bounds__(kJoinThreads)

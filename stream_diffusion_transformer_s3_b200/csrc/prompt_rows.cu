@@ -146,7 +146,8 @@ __device__ __forceinline__ void store8(char* at, const float (&v)[8]) {
 // 16 bytes found by division, 80 us with each group staying on its head (addresses advancing
 // by a row), 69 us with 16 elements a lane, 67 us with the norm weights in shared memory and
 // the registers of four CTAs per SM (two tokens in flight per lane: 73 us, four: 103 us, their
-// registers cost more threads).
+// registers cost more threads), 63 us (5.3 TB/s) with types and pairing as template arguments
+// and the weights laid out so that no two lanes of a read share a bank.
 enum {
   PAIR_OWN = 0,     // interleaved: pairs inside a chunk, tables in multiples of 4 pairs
   PAIR_LOCAL = 1,   // halves of the whole head: element i of both chunks
