@@ -372,7 +372,7 @@ ZDIT_API zdit_status zdit_gemm_bf16(const void* A, const void* B, float* C, int6
  * of the library.  They return once their work is queued on the stream, need the tensors'
  * device to be the current one, and may be captured into graphs; zdit_profile_begin
  * records them under the kernel kinds that they resemble (rope_table, norm_modulate,
- * attention, gemm_other). */
+ * attention, gemm_embed_final). */
 
 /* Element types of the buffers whose type a call leaves open. */
 enum { ZDIT_T_BF16 = 0, ZDIT_T_F32 = 1 };
@@ -413,8 +413,8 @@ typedef struct {
  *               precision, so positions far past 2^24 keep their phase)
  *   rotary_dim  even, 2..512;  theta >= 1 (frequencies at most 1)
  *   scaling     NULL: NONE with magnitude 1
- * T == 0 does nothing.  Errors: ZDIT_ERR_INVALID_ARG (null pointers, theta, scaling
- * values), ZDIT_ERR_SHAPE, ZDIT_ERR_ALIGNMENT (cos_out, sin_out 16-byte aligned),
+ * T == 0 does nothing.  Errors: ZDIT_ERR_INVALID_ARG (null pointers, cos_out and sin_out the
+ * same, theta, scaling values), ZDIT_ERR_SHAPE, ZDIT_ERR_ALIGNMENT (cos_out, sin_out 16-byte aligned),
  * ZDIT_ERR_CUDA. */
 ZDIT_API zdit_status zdit_rope_table_scaled(const int32_t* pos, int64_t T, int32_t rotary_dim, float theta,
                                             const zdit_rope_scaling* scaling, float* cos_out, float* sin_out,
@@ -428,8 +428,8 @@ enum { ZDIT_ROPE_INTERLEAVED = 0, ZDIT_ROPE_HALF = 1 };
  *   (a, b) <- (a cos_i - b sin_i, a sin_i + b cos_i) for pair i < rotary_dim / 2
  * computed in fp32 and rounded once; elements past rotary_dim are only normed.
  *   q, k          in_dtype, T rows of n_q / n_k heads; n_k == 0: queries only
- *   q_out, k_out  out_dtype.  The same buffer as the input (pointer, strides and type
- *                 alike: in place) or one that does not overlap it.
+ *   q_out, k_out  out_dtype.  The same buffer as its input (pointer, strides and type
+ *                 alike: in place), otherwise overlapping neither input nor one another.
  *   head_dim      a multiple of 8, 8..256
  *   w_q, w_k      device fp32 [head_dim] or NULL, 16-byte aligned
  *   cos, sin      device fp32 [T, rotary_dim / 2], 16-byte aligned; may be NULL if

@@ -417,6 +417,7 @@ ZDIT_API zdit_status zdit_rope_table_scaled(const int32_t* pos, int64_t T, int32
   if (T > INT64_MAX / (8 * kMaxPairs)) return ZDIT_ERR_SHAPE;
   if (!aligned16(cos_out) || !aligned16(sin_out) || (reinterpret_cast<uintptr_t>(pos) & 3)) return ZDIT_ERR_ALIGNMENT;
   if (T == 0) return ZDIT_OK;
+  if (cos_out == sin_out) return ZDIT_ERR_INVALID_ARG;
   if (!device_ok()) return ZDIT_ERR_UNSUPPORTED;
   RopeScaledParams p;
   p.pos = pos; p.T = T; p.pairs = rotary_dim / 2; p.factor = sc.factor;
@@ -467,6 +468,8 @@ ZDIT_API zdit_status zdit_qk_norm_rope(const zdit_qk_norm_rope_args* a, void* st
          (n > 1 && hs[i]->head_stride != hs[i + 1]->head_stride)))
       return ZDIT_ERR_INVALID_ARG;
   }
+  if (a->n_k > 0 && (a->q_out.ptr == a->k_out.ptr || a->q_out.ptr == a->k.ptr || a->k_out.ptr == a->q.ptr))
+    return ZDIT_ERR_INVALID_ARG;
   if (!aligned16(a->w_q) || !aligned16(a->w_k) || !aligned16(a->cos) || !aligned16(a->sin)) return ZDIT_ERR_ALIGNMENT;
   if (a->T == 0) return ZDIT_OK;
   if (!device_ok()) return ZDIT_ERR_UNSUPPORTED;

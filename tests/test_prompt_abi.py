@@ -71,6 +71,18 @@ def test_qk_norm_rope_refusals(kw, code):
     assert Z.lib().zdit_qk_norm_rope(C.byref(qk_args(**kw)), None) == code
 
 
+@pytest.mark.parametrize("kw", [
+    dict(k_out=Z.Heads(2 * P, 256, 128)), dict(q_out=Z.Heads(3 * P, 512, 128)), dict(k_out=Z.Heads(P, 256, 128)),
+])
+def test_qk_norm_rope_refuses_one_buffer_for_two_heads(kw):
+    # both outputs, or an output and the other input, in one place
+    assert Z.lib().zdit_qk_norm_rope(C.byref(qk_args(**kw)), None) == INVALID
+
+
+def test_rope_table_scaled_refuses_one_buffer_for_both_tables():
+    assert rope(cos=P, sin=P, T=4) == INVALID
+
+
 def test_qk_norm_rope_refuses_null():
     assert Z.lib().zdit_qk_norm_rope(None, None) == INVALID
 
