@@ -660,3 +660,70 @@ def test_prompt_rows_of_a_later_call_match_the_whole_prompt():
     ref, bound = attention_ref(q, k, v, [n], [n], [0], True, hd ** -0.5)
     check(whole, ref, bound, "whole")
     check(parts, ref, bound, "in parts")
+
+
+def test_prompt_layers_on_two_streams_at_once():
+    # eager calls and captured graphs of two streams, each with buffers of its own
+    L = Layer(128, 4, 2, 64)
+    runs = []
+    for i, q_len in enumerate([(300, 7, 41), (1, 900)]):
+        T = sum(q_len)
+        x16 = rnd(30 + i, T, L.D)
+        pos = torch.cat([torch.arange(n) for n in q_len]).to(device="cuda", dtype=torch.int32)
+        buf = (torch.empty(T, 8 * 64, device="cuda", dtype=torch.bfloat16), torch.empty(T, 32, device="cuda"),
+               torch.empty(T, 32, device="cuda"), torch.empty(T, 4, 64, device="cuda", dtype=torch.bfloat16),
+               workspace(Z.PromptBatch(q_len), 4, 2, 64))
+        x = x16.float()
+        alone = torch.empty_like(x)
+        L.run(x, x16, pos, q_len, alone, buf)
+        runs.append((torch.cuda.Stream(), x, x16, pos, q_len, buf, alone, [torch.zeros_like(x) for _ in range(8)]))
+    torch.cuda.synchronize()
+    for r in range(8):
+        for s, x, x16, pos, q_len, buf, alone, outs in runs:
+            with torch.cuda.stream(s):
+                L.run(x, x16, pos, q_len, outs[r], buf)
+    torch.cuda.synchronize()
+    for *_, alone, outs in runs:
+        assert all(torch.equal(o, alone) for o in outs)
+    graphs = []
+    for s, x, x16, pos, q_len, buf, alone, outs in runs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            L.run(x, x16, pos, q_len, outs[0], buf)
+        outs[0].zero_()
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for g, (s, *_) in zip(graphs, runs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for *_, alone, outs in runs:
+        assert torch.equal(outs[0], alone)
+    assert Z.zdit_device_status() == 0
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_prompt_attention_many_sequences_on_the_same_keys(hd):
+    # the largest batch; every other sequence continues the same prefix, the rest have their own keys
+    H, Hkv = 4, 2
+    q_len = [1 + b % 5 for b in range(128)]
+    kv_len = [200 + b % 5 if b % 2 == 0 else 1 + 3 * b for b in range(128)]
+    starts = [0 if b % 2 == 0 else 10 * b for b in range(128)]
+    q = rnd(1, sum(q_len), H, hd)
+    rows = max(s + n for s, n in zip(starts, kv_len))
+    k, v = rnd(2, rows, Hkv, hd), rnd(3, rows, Hkv, hd)
+    o = torch.empty_like(q)
+    b = Z.PromptBatch(q_len, kv_len, starts)
+    Z.zdit_prompt_attention(q, k, v, o, b, workspace(b, H, Hkv, hd))
+    ref, bound = attention_ref(q, k, v, q_len, kv_len, starts, True, hd ** -0.5)
+    check(o, ref, bound, "128 sequences")
+
+
+def test_prompt_attention_without_query_rows_writes_nothing():
+    q = rnd(1, 3, 2, 64)
+    k = rnd(2, 9, 2, 64)
+    o = torch.full_like(q, 5.0)
+    Z.zdit_prompt_attention(q, k, k.clone(), o, Z.PromptBatch([0, 0], [4, 5]))
+    torch.cuda.synchronize()
+    assert (o == 5).all() and Z.zdit_device_status() == 0
