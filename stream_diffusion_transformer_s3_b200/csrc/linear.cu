@@ -8,9 +8,12 @@
 // over the SMs.  The parts of one tile are a cluster: each leaves its fp32 partial tile in
 // its own shared memory and every CTA adds up its share of the rows over the cluster's
 // shared memory, in rank order (the result does not depend on timing, and there is no
-// workspace to clear or share).  That traffic runs at ~2 TB/s over the GPU, so the more rows
-// the fewer parts; sending the rows to their owners with bulk copies instead is no faster
-// (133 x 9728 x 2560 19.3 against 18.0 us, 1 x 2560 x 4096 8.4 against 7.5).
+// workspace to clear or share).  At 133 x 9728 x 2560 (17.8 us) making the products takes 12 us,
+// moving them to shared memory 1.4, and adding them up and storing 4, of which the distance of
+// the peers' memory is 1.2; so the more rows the fewer parts.  Sending the rows to their owners
+// with bulk copies instead is no faster (19.3 against 18.0 us, 1 x 2560 x 4096 8.4 against 7.5).
+// Bias and residual are fetched while the products are made (19.1 -> 17.8 us with the
+// accumulator read 16 instead of 8 columns at a time; 2048 deep, 2560 wide, 64 rows: 8.3 -> 7.7).
 //
 // Warp roles (320 threads): warp 0 loads (TMA ring), warp 1 issues the MMAs, warps 2-9 move
 // the accumulator (TMEM lane = feature, column = row of a).
@@ -213,17 +216,38 @@ __global__ void __launch_bounds__(THREADS)
     int dummy = 0;
     mbar_wait(done, 0, &dummy);
   }
-  __syncthreads();  // (the other warps wait here, not in a polling loop)
+  // split: rows rank, rank + split, ... of the tile are this CTA's, 4 features per lane.  What
+  // the first of them need beside the products is fetched while the products are made.
+  constexpr int kRows = 2;
   const int rows = min(p.row_tile, p.M - r0);
+  const int f4 = f0 + lane * 4;
+  int r = rank + (warp - 2) * p.split;
+  float bias[4] = {}, res[kRows][4] = {};
+  auto fetch = [&](int row) {
+    if (p.e.residual == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (row + i * EPI_WARPS * p.split < rows)
+        linear_residual4(p.e, r0 + row + i * EPI_WARPS * p.split, f4, p.N, res[i]);
+  };
   const int lg = warp & 3, half = (warp - 2) >> 2;  // TMEM lane group; which of its two warps
+  const int f1 = f0 + lg * 32 + lane;               // unsplit: the lane's one feature
+  if (warp >= 2 && p.split == 1) {
+    if (p.e.bias != nullptr && f1 < p.N) bias[0] = __ldg(p.e.bias + f1);
+  } else if (warp >= 2) {
+    if (p.e.bias != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (f4 + j < p.N) bias[j] = __ldg(p.e.bias + f4 + j);
+    }
+    fetch(r);
+  }
+  __syncthreads();  // (the other warps wait here, not in a polling loop)
   const uint32_t t0 = tmem + ((uint32_t)(lg * 32) << 16);
   if (p.split == 1) {
     // straight from the accumulator, 8 rows of one feature per lane at a time
     if (warp >= 2 && !abort_flag) {
       tc_fence_after();
-      const int f = f0 + lg * 32 + lane;
-      const bool f_ok = f < p.N;
-      const float bias = p.e.bias != nullptr && f_ok ? __ldg(p.e.bias + f) : 0.f;
       for (int c = half * 8; c < rows; c += 16) {
         uint32_t t[8];
         __syncwarp();
@@ -231,10 +255,10 @@ __global__ void __launch_bounds__(THREADS)
         tmem_ld_wait();
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(t[j]) + bias;
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(t[j]) + bias[0];
         linear_act_all<8>(v, p.e.act);
         const int64_t row = r0 + c;
-        if (f_ok) finish_rows(p.e, row * p.e.ld_res + f, row * p.e.ld_out + f, min(8, rows - c), v);
+        if (f1 < p.N) finish_rows(p.e, row * p.e.ld_res + f1, row * p.e.ld_out + f1, min(8, rows - c), v);
       }
     }
     tc_fence_before();
@@ -245,28 +269,25 @@ __global__ void __launch_bounds__(THREADS)
     if (warp >= 2 && !abort_flag) {
       tc_fence_after();
       float* col = part + lg * 32 + lane;
-      for (int c = half * 8; c < rows; c += 16) {
-        uint32_t t[8];
-        tmem_ld8(t0 + c, t);
+      for (int c = half * 16; c < rows; c += 32) {
+        uint32_t t[16];
+        tmem_ld16(t0 + c, t);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) col[(c + j) * FT] = __uint_as_float(t[j]);
+        for (int j = 0; j < 16; ++j) col[(c + j) * FT] = __uint_as_float(t[j]);
       }
     }
     tc_fence_before();
     __syncwarp();
     cluster_sync();  // partial tiles of the whole cluster are visible
     if (warp >= 2 && !abort_flag) {
-      // rows rank, rank + split, ... of the tile: a warp adds up kRows of them at a time, 4
-      // features per lane, all loads of the cluster in flight at once
-      const int f = f0 + lane * 4;
+      // a warp adds up kRows rows at a time, all loads of the cluster in flight at once
       const uint32_t base = smem_u32(part) + lane * 16;
-      constexpr int kRows = 2;
       const int step = EPI_WARPS * p.split;
       uint32_t peer[kMaxSplit];
 #pragma unroll
       for (int s = 0; s < kMaxSplit; ++s) peer[s] = map_cluster(base, s < p.split ? s : rank);
-      for (int r = rank + (warp - 2) * p.split; r < rows; r += kRows * step) {
+      for (; r < rows; r += kRows * step) {
         float4 q[kRows][kMaxSplit];
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
@@ -282,8 +303,14 @@ __global__ void __launch_bounds__(THREADS)
           for (int s = 1; s < kMaxSplit; ++s) {
             v[0] += q[i][s].x; v[1] += q[i][s].y; v[2] += q[i][s].z; v[3] += q[i][s].w;
           }
-          linear_finish<4>(p.e, r0 + r + i * step, f, p.N, v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] += bias[j];
+          linear_act_all<4>(v, p.e.act);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] += res[i][j];
+          linear_store<4>(p.e, r0 + r + i * step, f4, p.N, v);
         }
+        fetch(r + kRows * step);
       }
     }
     __syncwarp();
