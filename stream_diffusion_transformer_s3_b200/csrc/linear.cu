@@ -135,6 +135,26 @@ __global__ void __launch_bounds__(THREADS)
   const int slice_bytes = W_TILE + p.row_tile * BK * 2;
   const int stage_bytes = p.group * slice_bytes;
 
+  // The loads of this CTA, by thread 0.  (Stage and phase are counted: a division by the
+  // run-time ring depth would cost more than the slice it serves.)
+  int st = 0, k_at = k_lo * BK, left = n;
+  uint32_t phase = 0, armed = 0;
+  uint8_t* dst = smem;
+  auto load_stage = [&]() {
+    const int g = min(p.group, left);
+    mbar_arrive_expect_tx(&full[st], g * slice_bytes);
+    for (int j = 0; j < g; ++j) tma_load_2d(dst + j * slice_bytes, &tmW, &full[st], k_at + j * BK, f0);
+    for (int j = 0; j < g; ++j) tma_load_2d(dst + j * slice_bytes + W_TILE, &tmA, &full[st], k_at + j * BK, r0);
+    armed = (armed & ~(1u << st)) | (phase << st) | (0x10000u << st);
+    left -= g;
+    k_at += g * BK;
+    dst += stage_bytes;
+    if (++st == p.stages) {
+      st = 0;
+      phase ^= 1;
+      dst = smem;
+    }
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
@@ -143,10 +163,10 @@ __global__ void __launch_bounds__(THREADS)
     mbar_init(done, 1);
     abort_flag = 0;
     fence_barrier_init();
-  }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmA);
+    griddep_wait();
+    // this thread made the barriers: its first stage need not wait for the others (0.1 to 0.2 us
+    // of every call; the whole ring before the others start costs up to 0.6 us instead)
+    load_stage();
   }
   if (warp == 1) tmem_alloc(&tmem_slot, p.tmem_cols);
   tc_fence_before();
@@ -157,27 +177,7 @@ __global__ void __launch_bounds__(THREADS)
   griddep_trigger();
 
   if (warp == 0 && lane == 0) {
-    // (stage and phase are counted: a division by the run-time ring depth would cost more
-    // than the slice it serves)
-    int st = 0, k = k_lo * BK, left = n;
-    uint32_t phase = 0, armed = 0;
-    uint8_t* dst = smem;
-    while (left > 0) {
-      if (!mbar_wait(&empty[st], phase ^ 1, &abort_flag, p.err)) break;
-      const int g = min(p.group, left);
-      mbar_arrive_expect_tx(&full[st], g * slice_bytes);
-      for (int j = 0; j < g; ++j) tma_load_2d(dst + j * slice_bytes, &tmW, &full[st], k + j * BK, f0);
-      for (int j = 0; j < g; ++j) tma_load_2d(dst + j * slice_bytes + W_TILE, &tmA, &full[st], k + j * BK, r0);
-      armed = (armed & ~(1u << st)) | (phase << st) | (0x10000u << st);
-      left -= g;
-      k += g * BK;
-      dst += stage_bytes;
-      if (++st == p.stages) {
-        st = 0;
-        phase ^= 1;
-        dst = smem;
-      }
-    }
+    while (left > 0 && mbar_wait(&empty[st], phase ^ 1, &abort_flag, p.err)) load_stage();
     if (abort_flag) {  // let copies in flight land before shared memory is released
       int dummy = 0;
       for (int i = 0; i < p.stages; ++i)
@@ -187,8 +187,7 @@ __global__ void __launch_bounds__(THREADS)
     const uint32_t idesc = idesc_bf16_f32(FT, p.row_tile);
     const uint64_t w0 = sdesc_kmajor_sw128(smem_u32(smem));
     const uint64_t stage_desc = stage_bytes >> 4, slice_desc = slice_bytes >> 4;  // linear in the address
-    int st = 0, left = n;
-    uint32_t phase = 0, acc = 0;
+    uint32_t acc = 0;
     uint64_t ws = w0;
     while (left > 0) {
       if (!mbar_wait(&full[st], phase, &abort_flag, p.err)) break;
