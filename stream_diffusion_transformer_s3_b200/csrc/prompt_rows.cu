@@ -328,10 +328,11 @@ __global__ void __launch_bounds__(kQkThreads, 4) qk_norm_rope_kernel(const QkPar
     } else {
       float* x = xs + (threadIdx.x / G) * (G * 16);
       __syncwarp();  // the previous token's readers are done
+      // (only lanes that hold elements: lane l >= C would write where lane l - C's second chunk is)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[ea + i] = a[i];
-        if (eb + i < G * 16) x[eb + i] = b[i];
+        if (lane < chunks) x[ea + i] = a[i];
+        if (has_b) x[eb + i] = b[i];
       }
       __syncwarp();
       if (live) {

@@ -727,3 +727,14 @@ def test_prompt_attention_without_query_rows_writes_nothing():
     Z.zdit_prompt_attention(q, k, k.clone(), o, Z.PromptBatch([0, 0], [4, 5]))
     torch.cuda.synchronize()
     assert (o == 5).all() and Z.zdit_device_status() == 0
+
+
+# ------------------------------------------------------------------ rotations past a head's first chunks
+@pytest.mark.parametrize("T", [1, 37])
+@pytest.mark.parametrize("src,dst", [("b", "b"), ("f", "f")])
+@pytest.mark.parametrize("hd,rot", [(24, 24), (40, 40), (72, 72), (80, 48), (80, 80), (88, 88), (96, 64), (104, 104),
+                                    (112, 72), (192, 128), (200, 200), (248, 136)])
+def test_qk_norm_rope_halves_past_the_first_chunks(hd, rot, T, src, dst):
+    # heads that leave lanes of their group without elements, partners on both sides of the
+    # element where the lanes' second chunks begin
+    test_qk_norm_rope(T, 3, 2, hd, rot, src, dst, True, Z.ROPE_HALF)
