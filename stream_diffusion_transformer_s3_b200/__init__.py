@@ -507,7 +507,7 @@ def prompt_attention_workspace_bytes(batch: PromptBatch, n_heads, n_kv_heads, he
 
 def zdit_prompt_attention(q, k, v, o, batch: PromptBatch, workspace=None, causal=True, scale=0.0, stream=None):
     """Attention of packed prompts: q, o [rows, n_heads, head_dim], k, v [rows, n_kv_heads,
-    head_dim], bf16, any row and head strides.  workspace: a uint8 tensor of
+    head_dim], bf16, any row and head strides.  workspace: a contiguous uint8 tensor of
     prompt_attention_workspace_bytes (None when that is 0)."""
     w = "zdit_prompt_attention"
     bf = _th().bfloat16
@@ -521,6 +521,8 @@ def zdit_prompt_attention(q, k, v, o, batch: PromptBatch, workspace=None, causal
         raise ValueError(f"{w}: o must have q's heads, and all the same head_dim")
     if R < batch.q_rows or Ro < batch.q_rows or S < batch.kv_rows:
         raise ValueError(f"{w}: the batch needs {batch.q_rows} rows of q and o and {batch.kv_rows} of k and v")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError(f"{w}: workspace must be contiguous")
     s = _launch_stream(w, stream, q, k, v, o, workspace)
     a = batch.args(H, Hkv, hd, causal, scale, hq + hk + hv + ho)
     pw, nw = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())

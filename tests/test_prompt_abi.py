@@ -215,3 +215,15 @@ def test_binding_refuses_what_the_structs_cannot_carry():
         Z.zdit_rope_table_scaled(torch.zeros(3), 64, 1e4, torch.zeros(3, 32), torch.zeros(3, 32))
     with pytest.raises(ValueError):
         Z.zdit_qk_norm_rope(q, k, q, k, None, None, torch.zeros(3, 64), torch.zeros(3, 64), 128)  # rows differ
+
+
+def test_binding_refuses_a_workspace_with_less_memory_than_elements():
+    # an expanded or strided tensor names more bytes than it holds from its first on
+    b16 = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    q, k = b16(1, 32, 128), b16(8192, 8, 128)
+    batch = Z.PromptBatch([1], [8192])
+    need = Z.prompt_attention_workspace_bytes(batch, 32, 8, 128)
+    assert need > 0
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(need), torch.zeros(2 * need, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            Z.zdit_prompt_attention(q, k, k.clone(), q.clone(), batch, ws)
