@@ -620,18 +620,33 @@ zdit_status launch_epi(const CUtensorMap& ta, const CUtensorMap& tb, const KPara
 
 }  // namespace
 
-bool make_tmap_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld_elems,
-                       uint32_t box_rows, uint32_t box_cols) {
+// bf16 tensor map with 128-byte swizzle; dims, strides (bytes) and box innermost first.
+static bool encode_tmap_bf16(CUtensorMap* m, uint32_t rank, const void* ptr, const cuuint64_t* dims,
+                             const cuuint64_t* strides, const cuuint32_t* box) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {ld_elems * 2};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint32_t estr[3] = {1, 1, 1};
+  auto encode = [&] {
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    // The first call of this host thread: runtime calls make the device's context current by
+    // themselves, this driver call does not.
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
+  }
   return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld_elems,
+                       uint32_t box_rows, uint32_t box_cols) {
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {ld_elems * 2};
+  const cuuint32_t box[2] = {box_cols, box_rows};
+  return encode_tmap_bf16(m, 2, ptr, dims, strides, box);
 }
 
 // Rows of heads: element (d, head, row) at ptr + (row * row_stride + head * head_stride + d)
@@ -639,16 +654,10 @@ bool make_tmap_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t 
 // consecutive 128-byte rows (row-major over rows, heads inside), 128-byte swizzled.
 bool make_tmap_bf16_heads(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t heads, uint64_t head_dim,
                           uint64_t row_stride, uint64_t head_stride, uint32_t box_heads, uint32_t box_rows) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[3] = {head_dim, heads, rows};
-  cuuint64_t strides[2] = {(heads > 1 ? head_stride : head_dim) * 2, (rows > 1 ? row_stride : head_dim) * 2};
-  cuuint32_t box[3] = {64, box_heads, box_rows};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  const cuuint64_t dims[3] = {head_dim, heads, rows};
+  const cuuint64_t strides[2] = {(heads > 1 ? head_stride : head_dim) * 2, (rows > 1 ? row_stride : head_dim) * 2};
+  const cuuint32_t box[3] = {64, box_heads, box_rows};
+  return encode_tmap_bf16(m, 3, ptr, dims, strides, box);
 }
 
 // ZDIT_GEMM_SINGLE_CTA=1 in the environment selects the single-CTA kernel for every

@@ -738,3 +738,48 @@ def test_qk_norm_rope_halves_past_the_first_chunks(hd, rot, T, src, dst):
     # heads that leave lanes of their group without elements, partners on both sides of the
     # element where the lanes' second chunks begin
     test_qk_norm_rope(T, 3, 2, hd, rot, src, dst, True, Z.ROPE_HALF)
+
+
+# ------------------------------------------------------------------ host threads
+@pytest.mark.parametrize("op", ["rope", "qk", "attention", "linear", "linear many rows", "gemm", "joint attention"])
+def test_first_call_of_a_host_thread(op):
+    # a thread on which nothing has touched the device yet: no torch call, no cudaSetDevice
+    from threading import Thread
+    T, H, hd = 40, 2, 128
+    q, k, v = (rnd(i, T, H, hd) for i in (1, 2, 3))
+    cos, sin = tables(T, hd)
+    M = 4096 if op == "linear many rows" else 3
+    a, w = rnd(5, M, 256), rnd(6, 4096, 256)
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    out = {"rope": (T, hd // 2), "linear": (M, 4096), "linear many rows": (M, 4096), "gemm": (M, 4096)}.get(op, (T, H, hd))
+    ty = torch.float32 if len(out) == 2 else torch.bfloat16
+    o, want = (torch.zeros(out, device="cuda", dtype=ty) for _ in range(2))
+    o2, batch, one = torch.zeros_like(o), Z.PromptBatch([T]), Z.DeviceVarlen([0, T])
+    stream = torch.cuda.current_stream()
+    calls = {
+        "rope": lambda o: Z.zdit_rope_table_scaled(pos, hd, 1e4, o, o2, stream=stream),
+        "qk": lambda o: Z.zdit_qk_norm_rope(q, None, o, None, None, None, cos, sin, hd, stream=stream),
+        "attention": lambda o: Z.zdit_prompt_attention(q, k, v, o, batch, causal=False, stream=stream),
+        "linear": lambda o: Z.zdit_linear(a, w, o, stream=stream),
+        "linear many rows": lambda o: Z.zdit_linear(a, w, o, stream=stream),
+        "gemm": lambda o: Z.zdit_gemm_bf16(a, w, o, stream=stream),
+        "joint attention": lambda o: Z.zdit_joint_attention(*(x.view(T, -1) for x in (q, k, v, o)), one, H,
+                                                            stream=stream),
+    }
+    assert Z.prompt_attention_workspace_bytes(batch, H, H, hd, False) == 0
+    calls[op](want)
+    torch.cuda.synchronize()
+    failed = []
+
+    def work():
+        try:
+            calls[op](o)
+        except Exception as e:
+            failed.append(e)
+
+    t = Thread(target=work)
+    t.start()
+    t.join()
+    assert not failed
+    assert Z.zdit_device_status() == 0
+    assert torch.equal(o, want)
