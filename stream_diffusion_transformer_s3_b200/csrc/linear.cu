@@ -40,6 +40,8 @@ constexpr int kRing = 110 * 1024;    // shared memory of the ring: two CTAs fit 
 constexpr int kMaxStages = 8;
 constexpr int kMaxSplit = 8;         // portable cluster size
 constexpr int kMaxRowTile = 160;     // rows of a in one tile
+constexpr int kMaxSmem = 1024 + kRing;  // of any plan; the partial tiles lie over the idle ring
+static_assert(kMaxRowTile * FT * 4 <= kRing, "partial tile");
 
 struct FewParams {
   int M, N;
@@ -376,7 +378,9 @@ zdit_status launch_few(const zdit_linear_args& a, const LinearEpi& e, const FewP
   if (!make_tmap_bf16_2d(&tw, a.w, a.N, a.K, a.ldw, FT, BK) ||
       !make_tmap_bf16_2d(&ta, a.a, a.M, a.K, a.lda, f.row_tile, BK))
     return ZDIT_ERR_CUDA;
-  if (cudaFuncSetAttribute(linear_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem) != cudaSuccess)
+  // the opt-in is state of the context that all host threads share: always the largest, so that
+  // no call takes away what another one is about to launch with
+  if (cudaFuncSetAttribute(linear_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
     return ZDIT_ERR_CUDA;
   FewParams p;
   p.M = (int)a.M; p.N = (int)a.N; p.row_tile = f.row_tile; p.slices = (int)((a.K + BK - 1) / BK); p.split = f.split;

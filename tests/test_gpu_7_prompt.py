@@ -783,3 +783,34 @@ def test_first_call_of_a_host_thread(op):
     assert not failed
     assert Z.zdit_device_status() == 0
     assert torch.equal(o, want)
+
+
+def test_linear_from_host_threads_at_once():
+    # calls whose tiles need different amounts of shared memory, queued by several threads at
+    # once through the C call itself, so that they meet inside the library
+    import ctypes as C
+    from concurrent.futures import ThreadPoolExecutor
+    from threading import Barrier
+    N, K, rows = 256, 512, (1, 64, 144, 96) * 2
+    start, call = Barrier(len(rows), timeout=60), Z.lib().zdit_linear
+    w = rnd(2, N, K, scale=K ** -0.5)
+    a = [rnd(3 + M, M, K) for M in rows]
+    want, got = ([torch.zeros(M, N, device="cuda") for M in rows] for _ in range(2))
+    for x, o in zip(a, want):
+        Z.zdit_linear(x, w, o)
+    torch.cuda.synchronize()
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        g = Z.LinearArgs(M=rows[i], N=N, K=K, a=a[i].data_ptr(), lda=K, w=w.data_ptr(), ldw=K, out=got[i].data_ptr(),
+                         ld_out=N, out_dtype=1)
+        start.wait()
+        failed = sum(call(C.byref(g), stream.cuda_stream) != 0 for _ in range(5000))
+        stream.synchronize()
+        return failed
+
+    with ThreadPoolExecutor(len(rows)) as pool:
+        failed = list(pool.map(work, range(len(rows))))
+    assert failed == [0] * len(rows)
+    assert Z.zdit_device_status() == 0
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
