@@ -419,8 +419,8 @@ zdit_status launch_attention(const AttnArgs& a, cudaStream_t s) {
   if (!make_tmap_bf16_2d(&tk, a.k, a.T, cols, a.ldk, TILE, 64)) return ZDIT_ERR_CUDA;
   if (!make_tmap_bf16_2d(&tv, a.v, a.T, cols, a.ldv, TILE, 64)) return ZDIT_ERR_CUDA;
   // per launch: the opt-in belongs to the current context (see launch_epi)
-  if (cudaFuncSetAttribute(attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) != cudaSuccess)
-    return ZDIT_ERR_CUDA;
+  const cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e != cudaSuccess) return launch_status(e);
   AParams p;
   p.ldo = a.ldo;
   p.n_heads = a.n_heads;

@@ -603,19 +603,19 @@ zdit_status launch_epi(const CUtensorMap& ta, const CUtensorMap& tb, const KPara
   // The shared-memory opt-in is a property of the current context: set on every launch
   // (cheap, and legal inside stream capture) so a second device, or a context created
   // again after a reset, never launches without it.
+  cudaError_t e;
   if (pair) {
-    if (cudaFuncSetAttribute(gemm_pair_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             PairRing<pair_bk<EPI>()>::SMEM_BYTES) != cudaSuccess)
-      return ZDIT_ERR_CUDA;
-    launch_dependent(gemm_pair_kernel<EPI>, dim3(grid), dim3(THREADS), PairRing<pair_bk<EPI>()>::SMEM_BYTES, s, ta, tb,
-                     kp);
+    e = cudaFuncSetAttribute(gemm_pair_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             PairRing<pair_bk<EPI>()>::SMEM_BYTES);
+    if (e != cudaSuccess) return launch_status(e);
+    e = launch_dependent(gemm_pair_kernel<EPI>, dim3(grid), dim3(THREADS), PairRing<pair_bk<EPI>()>::SMEM_BYTES, s, ta,
+                         tb, kp);
   } else {
-    if (cudaFuncSetAttribute(gemm_tc_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) !=
-        cudaSuccess)
-      return ZDIT_ERR_CUDA;
-    launch_dependent(gemm_tc_kernel<EPI>, dim3(grid), dim3(THREADS), SMEM_BYTES, s, ta, tb, kp);
+    e = cudaFuncSetAttribute(gemm_tc_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e != cudaSuccess) return launch_status(e);
+    e = launch_dependent(gemm_tc_kernel<EPI>, dim3(grid), dim3(THREADS), SMEM_BYTES, s, ta, tb, kp);
   }
-  return cudaGetLastError() == cudaSuccess ? ZDIT_OK : ZDIT_ERR_CUDA;
+  return launch_status(e);
 }
 
 }  // namespace

@@ -150,6 +150,13 @@ bool profiling_on();
 // adds n to the launch counter (kernels replayed from a captured graph)
 void add_launches(int64_t n);
 
+// Status of a call whose launch or setup returned e.  The runtime keeps the error of a refused
+// launch until it is read: it is read here on every path, so that no later call reports it.
+inline zdit_status launch_status(cudaError_t e) {
+  const cudaError_t last = cudaGetLastError();
+  return e == cudaSuccess && last == cudaSuccess ? ZDIT_OK : ZDIT_ERR_CUDA;
+}
+
 // Device address of the library's latched device-error word on the current device.
 int* device_error_ptr();
 

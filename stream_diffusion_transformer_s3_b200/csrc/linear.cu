@@ -380,8 +380,9 @@ zdit_status launch_few(const zdit_linear_args& a, const LinearEpi& e, const FewP
     return ZDIT_ERR_CUDA;
   // the opt-in is state of the context that all host threads share: always the largest, so that
   // no call takes away what another one is about to launch with
-  if (cudaFuncSetAttribute(linear_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
-    return ZDIT_ERR_CUDA;
+  const cudaError_t opt_in =
+      cudaFuncSetAttribute(linear_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (opt_in != cudaSuccess) return launch_status(opt_in);
   FewParams p;
   p.M = (int)a.M; p.N = (int)a.N; p.row_tile = f.row_tile; p.slices = (int)((a.K + BK - 1) / BK); p.split = f.split;
   p.stages = f.stages; p.group = f.group; p.tmem_cols = f.tmem_cols; p.e = e; p.err = device_error_ptr();
@@ -402,8 +403,7 @@ zdit_status launch_few(const zdit_linear_args& a, const LinearEpi& e, const FewP
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, linear_few_kernel, tw, ta, p) != cudaSuccess) return ZDIT_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? ZDIT_OK : ZDIT_ERR_CUDA;
+  return launch_status(cudaLaunchKernelEx(&cfg, linear_few_kernel, tw, ta, p));
 }
 
 }  // namespace

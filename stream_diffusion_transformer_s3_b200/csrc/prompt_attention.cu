@@ -814,11 +814,11 @@ zdit_status launch_prompt(const CUtensorMap& tq, const CUtensorMap& tk, const CU
     p.heads_first = p.causal && items * p.n_kv < 9 * (int64_t)num_sms();
     const dim3 grid = p.heads_first ? dim3((unsigned)p.n_kv, (unsigned)items) : dim3((unsigned)items, (unsigned)p.n_kv);
     // per launch: the shared-memory opt-in belongs to the current context
-    if (cudaFuncSetAttribute(prompt_attn_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::SMEM) !=
-            cudaSuccess ||
-        launch_dependent(prompt_attn_kernel<HD>, grid, dim3(THREADS), Cfg<HD>::SMEM, s, tq, tk, tv, h.p, p) !=
-            cudaSuccess)
-      return ZDIT_ERR_CUDA;
+    cudaError_t e =
+        cudaFuncSetAttribute(prompt_attn_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::SMEM);
+    if (e == cudaSuccess)
+      e = launch_dependent(prompt_attn_kernel<HD>, grid, dim3(THREADS), Cfg<HD>::SMEM, s, tq, tk, tv, h.p, p);
+    if (e != cudaSuccess) return launch_status(e);
   }
   const int join = h.p.join0[h.p.n];
   if (join > 0) {
@@ -828,9 +828,9 @@ zdit_status launch_prompt(const CUtensorMap& tq, const CUtensorMap& tk, const CU
         join > 8 * num_sms()
             ? launch_dependent(prompt_join_kernel<HD, 1>, dim3((unsigned)((join + 3) / 4)), block, 0, s, h.p, p)
             : launch_dependent(prompt_join_kernel<HD, 4>, dim3((unsigned)join), block, 0, s, h.p, p);
-    if (e != cudaSuccess) return ZDIT_ERR_CUDA;
+    if (e != cudaSuccess) return launch_status(e);
   }
-  return cudaGetLastError() == cudaSuccess ? ZDIT_OK : ZDIT_ERR_CUDA;
+  return launch_status(cudaSuccess);
 }
 
 }  // namespace

@@ -437,7 +437,7 @@ ZDIT_API zdit_status zdit_rope_table_scaled(const int32_t* pos, int64_t T, int32
   ProfScope ps(PROF_ROPE, 0.0, 8.0 * T * p.pairs + 4.0 * T, s);
   const cudaError_t e = vec == 4 ? launch_dependent(rope_scaled_kernel<4>, grid, dim3(kRopeThreads), 0, s, p, tpr)
                                  : launch_dependent(rope_scaled_kernel<1>, grid, dim3(kRopeThreads), 0, s, p, tpr);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ZDIT_OK : ZDIT_ERR_CUDA;
+  return launch_status(e);
 }
 
 ZDIT_API zdit_status zdit_qk_norm_rope(const zdit_qk_norm_rope_args* a, void* stream) {
@@ -500,7 +500,7 @@ ZDIT_API zdit_status zdit_qk_norm_rope(const zdit_qk_norm_rope_args* a, void* st
   if (a->head_dim <= 64) e = launch_qk_group<4>(p, mode, s);
   else if (a->head_dim <= 128) e = launch_qk_group<8>(p, mode, s);
   else e = launch_qk_group<16>(p, mode, s);
-  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? ZDIT_OK : ZDIT_ERR_CUDA;
+  return launch_status(e);
 }
 
 }  // extern "C"

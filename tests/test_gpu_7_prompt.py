@@ -814,3 +814,53 @@ def test_linear_from_host_threads_at_once():
     assert failed == [0] * len(rows)
     assert Z.zdit_device_status() == 0
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+# ------------------------------------------------------------------ errors of the host
+@pytest.mark.parametrize("op", ["rope", "qk", "attention", "split attention", "linear", "linear many rows"])
+def test_a_refused_launch_does_not_fail_the_next_call(op):
+    # a launch on the default stream while a stream that waits for it is being captured is refused
+    # by the runtime, on the host; the capture is given up, another call and the same one are made
+    import ctypes as C
+    rt = C.CDLL("libcudart.so.12")
+    T, H, hd = (40, 2, 128) if op != "split attention" else (1, 2, 128)
+    n = T if T > 1 else 5000
+    q, k, v = rnd(1, T, H, hd), rnd(2, n, H, hd), rnd(3, n, H, hd)
+    cos, sin = tables(T, hd)
+    M = 4096 if op == "linear many rows" else 3
+    a, w = rnd(5, M, 256), rnd(6, 4096, 256)
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    lin, o, tab = torch.zeros(M, 4096, device="cuda"), torch.zeros_like(q), torch.zeros(2, T, hd // 2, device="cuda")
+    batch = Z.PromptBatch([T], [n])
+    ws = workspace(batch, H, H, hd)
+    assert (ws is not None) == (op == "split attention")
+    stream = torch.cuda.default_stream()
+    call = {
+        "rope": lambda: Z.zdit_rope_table_scaled(pos, hd, 1e4, tab[0], tab[1], stream=stream),
+        "qk": lambda: Z.zdit_qk_norm_rope(q, None, o, None, None, None, cos, sin, hd, stream=stream),
+        "attention": lambda: Z.zdit_prompt_attention(q, k, v, o, batch, ws, stream=stream),
+        "split attention": lambda: Z.zdit_prompt_attention(q, k, v, o, batch, ws, stream=stream),
+        "linear": lambda: Z.zdit_linear(a, w, lin, stream=stream),
+        "linear many rows": lambda: Z.zdit_linear(a, w, lin, stream=stream),
+    }[op]
+    call()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in (lin, o, tab)]
+    for x in (lin, o, tab):
+        x.zero_()
+    torch.cuda.synchronize()
+    side, graph = C.c_void_p(), C.c_void_p()
+    assert rt.cudaStreamCreate(C.byref(side)) == 0
+    assert rt.cudaStreamBeginCapture(side, 0) == 0  # global
+    try:
+        with pytest.raises(Z.ZditError, match="ZDIT_ERR_CUDA"):
+            call()
+    finally:
+        rt.cudaStreamEndCapture(side, C.byref(graph))  # (an error: the capture was invalidated)
+        rt.cudaGetLastError()
+        assert rt.cudaStreamDestroy(side) == 0
+    other = torch.empty(2, T, hd // 2, device="cuda")
+    Z.zdit_rope_table_scaled(pos, hd, 1e4, other[0], other[1], stream=stream)
+    call()
+    assert Z.zdit_device_status() == 0
+    assert all(torch.equal(x, y) for x, y in zip((lin, o, tab), want))
