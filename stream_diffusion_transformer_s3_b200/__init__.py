@@ -484,7 +484,14 @@ class PromptBatch:
     (None: packed one after the other)."""
 
     def __init__(self, q_len, kv_len=None, kv_start=None):
-        arr = lambda v: None if v is None else (C.c_int32 * len(v))(*[int(x) for x in v])
+        def arr(v):
+            if v is None:
+                return None
+            v = [int(x) for x in v]
+            if any(not -2**31 <= x < 2**31 for x in v):  # (ctypes would keep the low 32 bits)
+                raise ValueError("PromptBatch: lengths and first rows must fit 32 bits")
+            return (C.c_int32 * len(v))(*v)
+
         n = len(q_len)
         if any(v is not None and len(v) != n for v in (kv_len, kv_start)):
             raise ValueError("PromptBatch: q_len, kv_len and kv_start must have one entry per sequence")

@@ -227,3 +227,13 @@ def test_binding_refuses_a_workspace_with_less_memory_than_elements():
     for ws in (torch.zeros(1, dtype=torch.uint8).expand(need), torch.zeros(2 * need, dtype=torch.uint8)[::2]):
         with pytest.raises(ValueError, match="workspace"):
             Z.zdit_prompt_attention(q, k, k.clone(), q.clone(), batch, ws)
+
+
+@pytest.mark.parametrize("lens", [
+    dict(q_len=[1 << 32]), dict(q_len=[1], kv_len=[(1 << 32) + 5]), dict(q_len=[1], kv_len=[5], kv_start=[1 << 32]),
+    dict(q_len=[1], kv_len=[5], kv_start=[-(1 << 32)]), dict(q_len=[1 << 31]),
+])
+def test_batch_lengths_past_32_bits_are_refused(lens):
+    # (kept modulo 2^32 they would be other rows)
+    with pytest.raises(ValueError, match="PromptBatch"):
+        Z.PromptBatch(**lens)
