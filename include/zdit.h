@@ -504,7 +504,8 @@ ZDIT_API zdit_status zdit_prompt_attention(const zdit_prompt_attention_args* a, 
  *              (pointer, stride and type alike), otherwise does not overlap it
  *   out        out_dtype [M, N], row stride ld_out; does not overlap a, w or bias
  * Any M >= 0, N, K >= 1.  a and w 16-byte aligned with strides that are multiples of 8
- * elements (K need not be); bias, residual and out aligned to their element.  Columns past
+ * elements (K need not be); bias, residual and out aligned to their element.  The stride of a
+ * matrix of one row (M == 1, for w N == 1) is not used and may be anything.  Columns past
  * K and rows past M or N are never used.  Errors: ZDIT_ERR_INVALID_ARG, ZDIT_ERR_SHAPE,
  * ZDIT_ERR_ALIGNMENT, ZDIT_ERR_CUDA. */
 enum { ZDIT_ACT_NONE = 0, ZDIT_ACT_SILU = 1, ZDIT_ACT_GELU_TANH = 2, ZDIT_ACT_GELU = 3 };

@@ -414,12 +414,21 @@ using namespace zdit;
 
 extern "C" {
 
-ZDIT_API zdit_status zdit_linear(const zdit_linear_args* a, void* stream) {
-  if (a == nullptr || a->M < 0 || a->N < 0 || a->K < 0) return ZDIT_ERR_INVALID_ARG;
+ZDIT_API zdit_status zdit_linear(const zdit_linear_args* args, void* stream) {
+  if (args == nullptr || args->M < 0 || args->N < 0 || args->K < 0) return ZDIT_ERR_INVALID_ARG;
+  // the stride of a single row leads nowhere: any value is allowed, and one that keeps the
+  // tensor maps and the wide stores valid takes its place
+  const int64_t most = int64_t(1) << 30;
+  zdit_linear_args one = *args;
+  if (one.M == 1) {
+    one.lda = (std::min(one.K, most) + 7) / 8 * 8;
+    one.ld_out = one.ld_residual = (std::min(one.N, most) + 7) / 8 * 8;
+  }
+  if (one.N == 1) one.ldw = (std::min(one.K, most) + 7) / 8 * 8;
+  const zdit_linear_args* a = &one;
   if (a->act < ZDIT_ACT_NONE || a->act > ZDIT_ACT_GELU || a->out_dtype < 0 || a->out_dtype > 1 ||
       (a->residual && (a->residual_dtype < 0 || a->residual_dtype > 1)))
     return ZDIT_ERR_INVALID_ARG;
-  const int64_t most = int64_t(1) << 30;
   if (a->N < 1 || a->K < 1 || a->M > most || a->N > most || a->K > most || a->lda > most || a->ldw > most)
     return ZDIT_ERR_SHAPE;
   if (a->M == 0) return ZDIT_OK;
@@ -431,7 +440,7 @@ ZDIT_API zdit_status zdit_linear(const zdit_linear_args* a, void* stream) {
   if (((reinterpret_cast<uintptr_t>(a->a) | reinterpret_cast<uintptr_t>(a->w)) & 15) || a->lda % 8 || a->ldw % 8)
     return ZDIT_ERR_ALIGNMENT;
   if ((reinterpret_cast<uintptr_t>(a->bias) & 3) || oa % oe || (a->residual && ra % re)) return ZDIT_ERR_ALIGNMENT;
-  if (a->residual == a->out && (oe != re || (a->M > 1 && a->ld_residual != a->ld_out))) return ZDIT_ERR_INVALID_ARG;
+  if (a->residual == a->out && (oe != re || a->ld_residual != a->ld_out)) return ZDIT_ERR_INVALID_ARG;
   if (a->a == a->out || a->w == a->out) return ZDIT_ERR_INVALID_ARG;
   if (!device_ok()) return ZDIT_ERR_UNSUPPORTED;
   LinearEpi e{};

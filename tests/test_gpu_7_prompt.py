@@ -864,3 +864,22 @@ def test_a_refused_launch_does_not_fail_the_next_call(op):
     call()
     assert Z.zdit_device_status() == 0
     assert all(torch.equal(x, y) for x, y in zip((lin, o, tab), want))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 37, 100), (9, 1, 100), (1, 1, 3), (1, 5000, 260)])
+def test_linear_takes_a_single_row_of_any_stride(M, N, K):
+    # the stride of a matrix with one row leads nowhere: contiguous rows of K = 100, and views
+    # whose stride is smaller or larger than the row
+    pad = lambda seed, rows, scale=1.0: rnd(seed, rows, K, scale=scale) if rows == 1 else \
+        rnd(seed, rows, K + 12 + (4 - K) % 8, scale=scale)[:, :K]
+    a, w, x = pad(1, M), pad(2, N, K ** -0.5), rnd(3, M, N, dtype=torch.float32)
+    ref, e = linear_ref(a, w, None, Z.ACT_SILU, x)
+    want = None
+    for ld in ({K, 1, 4 * K + 1, 1 << 40} if M == 1 else {K}):
+        one = torch.as_strided(a, (1, K), (ld, 1)) if M == 1 else a
+        res = torch.as_strided(x, (1, N), (ld, 1)) if M == 1 else x
+        o = torch.full((M, N), 9.0, device="cuda")
+        Z.zdit_linear(one, w, torch.as_strided(o, (1, N), (ld, 1)) if M == 1 else o, act=Z.ACT_SILU, residual=res)
+        check(o, ref, e + 2.0 ** -24 * ref.abs(), f"single row {M}x{N}x{K} ld {ld}")
+        want = o if want is None else want
+        assert torch.equal(o, want)
