@@ -883,3 +883,89 @@ def test_linear_takes_a_single_row_of_any_stride(M, N, K):
         check(o, ref, e + 2.0 ** -24 * ref.abs(), f"single row {M}x{N}x{K} ld {ld}")
         want = o if want is None else want
         assert torch.equal(o, want)
+
+
+# ------------------------------------------------------------------ many rows and tokens
+def many_tiles(M, N):
+    """Whether a product has more 128-row tiles than the few-row kernel's two CTAs per SM: then
+    the GEMM takes it whatever the expected times are."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return -(-N // 128) * (1 if M <= 160 else -(-M // 128)) > 2 * sms
+
+
+# CTA pairs (M > 256): several tiles per pair, last tiles with one row or column of either CTA's
+# half and none of the other's, K shorter than a slice, K that ends in either half of one
+# single CTAs: M <= 256
+GEMM_SHAPES = [
+    (4100, 1500, 1003), (4225, 1345, 136), (8200, 600, 72), (40000, 100, 64), (5000, 1025, 5), (4700, 1152, 1),
+    (9000, 520, 193), (7, 38000, 130), (133, 38017, 64), (200, 19100, 300), (256, 19001, 1),
+]
+
+
+@pytest.mark.parametrize("M,N,K", GEMM_SHAPES)
+@pytest.mark.parametrize("act,bias,res,out", [
+    (Z.ACT_NONE, False, None, "f"),
+    (Z.ACT_SILU, True, None, "b"),
+    (Z.ACT_GELU, True, "f", "b"),
+    (Z.ACT_GELU_TANH, False, "b", "f"),
+])
+def test_linear_many_rows(M, N, K, act, bias, res, out):
+    assert many_tiles(M, N)
+    test_linear(M, N, K, act, bias, res, out)
+
+
+@pytest.mark.parametrize("M,N,K", [(4100, 1500, 1000), (4100, 1504, 264), (133, 38016, 256), (256, 19002, 64)])
+@pytest.mark.parametrize("ty", [torch.bfloat16, torch.float32])
+def test_linear_many_rows_residual_in_place(M, N, K, ty):
+    assert many_tiles(M, N)
+    test_linear_residual_in_place(M, N, K, ty)
+
+
+@pytest.mark.parametrize("M,N,K", [(145, 2560, 512), (160, 2560, 512), (160, 300, 2563), (152, 9728, 256)])
+@pytest.mark.parametrize("act,bias,res,out", [(Z.ACT_NONE, False, "f", "f"), (Z.ACT_GELU, True, "b", "b")])
+def test_linear_largest_row_tiles(M, N, K, act, bias, res, out):
+    test_linear(M, N, K, act, bias, res, out)
+
+
+@pytest.mark.parametrize("T", [4099, 16381])  # 2 and 8 tokens a group, the last group short
+@pytest.mark.parametrize("hd,rot,layout,src,norm", [
+    (128, 128, Z.ROPE_HALF, "b", True),           # pairs of a lane's own, both chunks
+    (128, 32, Z.ROPE_HALF, "b", True),            # pairs in another lane
+    (128, 72, Z.ROPE_HALF, "b", True),            # pairs through shared memory
+    (80, 80, Z.ROPE_HALF, "f", True),             # the same with lanes that hold nothing
+    (128, 128, Z.ROPE_INTERLEAVED, "f", True),    # pairs inside a chunk
+    (128, 30, Z.ROPE_INTERLEAVED, "b", False),    # 15 pairs
+])
+def test_qk_norm_rope_several_tokens_a_group(T, hd, rot, layout, src, norm):
+    test_qk_norm_rope(T, 32, 8, hd, rot, src, "b", norm, layout)
+
+
+@pytest.mark.parametrize("T,nq,nk,hd", [(9001, 32, 8, 64), (5003, 16, 4, 256)])  # groups of 4 and of 16 lanes
+@pytest.mark.parametrize("layout", [Z.ROPE_HALF, Z.ROPE_INTERLEAVED])
+def test_qk_norm_rope_several_tokens_other_groups(T, nq, nk, hd, layout):
+    test_qk_norm_rope(T, nq, nk, hd, hd, "b", "b", True, layout)
+    test_qk_norm_rope(T, nq, nk, hd, hd // 2 + 4, "b", "f", True, layout)
+
+
+@pytest.mark.parametrize("rot", [128, 72, 64])
+def test_qk_norm_rope_several_tokens_in_place(rot):
+    T, nq, nk, hd = 5003, 32, 8, 128
+    qkv = rnd(6, T, (nq + 2 * nk) * hd)
+    before = qkv.clone()
+    q, k = qkv[:, :nq * hd].view(T, nq, hd), qkv[:, nq * hd:(nq + nk) * hd].view(T, nk, hd)
+    w = 1 + 0.3 * rnd(1, hd, dtype=torch.float32)
+    cos, sin = tables(T, rot)
+    apart = [torch.empty(T, n, hd, device="cuda", dtype=torch.bfloat16) for n in (nq, nk)]
+    Z.zdit_qk_norm_rope(q, k, *apart, w, w, cos, sin, rot)
+    Z.zdit_qk_norm_rope(q, k, q, k, w, w, cos, sin, rot)
+    assert torch.equal(q, apart[0]) and torch.equal(k, apart[1])
+    assert torch.equal(qkv[:, (nq + nk) * hd:], before[:, (nq + nk) * hd:])
+
+
+@pytest.mark.parametrize("T,d,sc,first", [
+    (40003, 128, None, 0),                                                              # 16 rows a CTA and step
+    (20011, 22, Z.RopeScaling(Z.ROPE_SCALE_LINEAR, 4.0), 7),
+    (5001, 512, Z.RopeScaling(Z.ROPE_SCALE_YARN, 4.0, 32768.0, 32.0, 1.0, 1.1386), 98304),  # 4 rows
+])
+def test_rope_table_scaled_several_steps_a_cta(T, d, sc, first):
+    test_rope_table_scaled(T, d, 1e6, sc, first)
