@@ -329,32 +329,41 @@ struct FewPlan {
   uint32_t tmem_cols;
 };
 
-// Whether the few-row kernel takes a problem, and how.  Expected times in us, fitted to the
-// measured ones (within ~15%) over N x K of 500 x 5000 to 9728 x 2560 and 1 to 1024 rows:
-//   few rows   3.0 + slices per part * (0.30 + 0.0012 row_tile) * load
-//              (or the time to read w at 6.6 TB/s, if that is more) + the finish: 0.018 a row
+// Whether the few-row kernel takes a problem, and how.
+// One row tile (M <= 160): always.  From 256 to 152000 features by K of 64 to 10240 it is 0.98 to 7
+// times as fast as the GEMM where two CTAs per SM hold all of it, and 0.92 to 1.44 times where CTAs
+// follow one another (us few rows / GEMM: 1 row 256 x 10240 9 / 64, 24576 x 10240 80 / 138,
+// 33000 x 4096 44 / 63, 151936 x 2560 120 / 150; 160 rows 60000 x 1504 46 / 56; the losses: 100 rows
+// 60000 x 1504 42 / 39, 100000 x 136 22.6 / 21.0).
+// Otherwise by expected times in us:
+//   few rows   3.0 + slices per part * (0.30 + 0.0012 row_tile) * load + the finish: 0.018 a row
 //              unsplit, else 0.8 + 0.04 a row and CTA on the SM (the cluster's shared memory)
-//              load: 1 up to one CTA per SM, 1.2 up to 1.6 (two CTAs fill each other's gaps)
-//   GEMM       10 + 0.27 a slice and wave of its 256-wide tiles
-// e.g. us few rows / GEMM at 2560 x 4096: 16 rows 8 / 31, 133 rows 15 / 32, 512 rows 20 / 27;
-// 9728 x 2560: 13 / 24, 18 / 25, 57 / 35; 3840 x 10240: 16 / 69, 24 / 69, 48 / 56.
-// Clusters of 5 to 7 pack badly into the GPCs (6144 x 2560, 1 row: 6 parts 16.6 us, 3 parts 9.9).
+//              load: 1 up to one CTA per SM, 1.2 up to 1.6 (two CTAs fill each other's gaps);
+//              more are not taken (250 rows 24576 x 2560: 48 / 44, 500 rows 12000 x 2560: 50 / 40;
+//              300 rows 12000 x 2560, 1.9 CTAs per SM, would gain: 25 / 36)
+//   GEMM       10 + 0.34 a slice and wave of its 256-wide tiles (measured 0.26 to 0.44)
+// and in both no less than the time to read w at 6.6 TB/s.  Of 24 problems measured with 170 to 500
+// rows, 4000 x 4096 to 20000 x 1000, two are not given to the faster kernel and split within 10%: the
+// one above and 500 rows 4000 x 4096, 23 / 27.  us few rows / GEMM at 2560 x 4096: 512 rows 20 / 27;
+// 9728 x 2560: 512 rows 57 / 35; 3840 x 10240: 266 rows 48 / 56; 7680 x 10240: 256 rows 51 / 78.
+// Parts: 1 x 256 x 10240 45 us with one, 9 with eight; clusters of 5 to 7 pack badly into the GPCs
+// (6144 x 2560, 1 row: 6 parts 16.6 us, 3 parts 9.9).
 bool plan_few(int64_t M, int64_t N, int64_t K, FewPlan* f) {
-  const double sms = num_sms(), slices = (double)((K + BK - 1) / BK);
+  const double sms = num_sms(), slices = (double)((K + BK - 1) / BK), read_w = 2.0 * N * K / 6.6e6;
   const double wide_tiles = (double)(M > 256 ? (M + 255) / 256 : (M + 127) / 128) * ((N + 255) / 256);
-  const double gemm = 10.0 + 0.27 * slices * std::ceil(wide_tiles / (M > 256 ? sms / 2 : sms));
+  const double gemm = 10.0 + std::max(0.34 * slices * std::ceil(wide_tiles / (M > 256 ? sms / 2 : sms)), read_w);
   const int64_t row_tiles = M <= kMaxRowTile ? 1 : (M + 127) / 128;
   const double tiles = (double)((N + FT - 1) / FT) * row_tiles;
   f->row_tiles = (int)row_tiles;
   f->row_tile = (int)(((M + row_tiles - 1) / row_tiles + 15) / 16 * 16);
   f->split = 0;
-  double best = gemm;
+  double best = row_tiles == 1 ? INFINITY : gemm;
   const int sizes[] = {1, 2, 3, 4, 8};
   for (const int s : sizes) {
     const double ctas = tiles * s / sms;  // per SM
-    if (ctas > 1.63 || (s > 1 && slices < 2 * s)) break;
-    const double stream = std::max(std::ceil(slices / s) * (0.30 + 0.0012 * f->row_tile) * (ctas <= 1 ? 1.0 : 1.2),
-                                   2.0 * N * K / 6.6e6);
+    if ((ctas > 1.63 && (s > 1 || row_tiles > 1)) || (s > 1 && slices < 2 * s)) break;
+    const double stream =
+        std::max(std::ceil(slices / s) * (0.30 + 0.0012 * f->row_tile) * (ctas <= 1 ? 1.0 : 1.2), read_w);
     const double finish = s == 1 ? 0.018 * f->row_tile : 0.8 + 0.04 * f->row_tile * std::max(1.0, ctas);
     if (3.0 + stream + finish < best) {
       best = 3.0 + stream + finish;

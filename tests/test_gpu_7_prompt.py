@@ -887,10 +887,10 @@ def test_linear_takes_a_single_row_of_any_stride(M, N, K):
 
 # ------------------------------------------------------------------ many rows and tokens
 def many_tiles(M, N):
-    """Whether a product has more 128-row tiles than the few-row kernel's two CTAs per SM: then
-    the GEMM takes it whatever the expected times are."""
+    """Whether a product has several row tiles and more tiles than the few-row kernel's two CTAs
+    per SM: then the GEMM takes it whatever the expected times are."""
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    return -(-N // 128) * (1 if M <= 160 else -(-M // 128)) > 2 * sms
+    return M > 160 and -(-N // 128) * -(-M // 128) > 2 * sms
 
 
 # CTA pairs (M > 256): several tiles per pair, last tiles with one row or column of either CTA's
@@ -898,7 +898,7 @@ def many_tiles(M, N):
 # single CTAs: M <= 256
 GEMM_SHAPES = [
     (4100, 1500, 1003), (4225, 1345, 136), (8200, 600, 72), (40000, 100, 64), (5000, 1025, 5), (4700, 1152, 1),
-    (9000, 520, 193), (7, 38000, 130), (133, 38017, 64), (200, 19100, 300), (256, 19001, 1),
+    (9000, 520, 193), (161, 19300, 130), (250, 30001, 64), (200, 19100, 300), (256, 19001, 1),
 ]
 
 
@@ -914,11 +914,18 @@ def test_linear_many_rows(M, N, K, act, bias, res, out):
     test_linear(M, N, K, act, bias, res, out)
 
 
-@pytest.mark.parametrize("M,N,K", [(4100, 1500, 1000), (4100, 1504, 264), (133, 38016, 256), (256, 19002, 64)])
+@pytest.mark.parametrize("M,N,K", [(4100, 1500, 1000), (4100, 1504, 264), (193, 20000, 256), (256, 19002, 64)])
 @pytest.mark.parametrize("ty", [torch.bfloat16, torch.float32])
 def test_linear_many_rows_residual_in_place(M, N, K, ty):
     assert many_tiles(M, N)
     test_linear_residual_in_place(M, N, K, ty)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 38000, 130), (7, 24577, 300), (133, 38017, 64), (160, 45000, 72)])
+@pytest.mark.parametrize("act,bias,res,out", [(Z.ACT_NONE, False, "f", "f"), (Z.ACT_GELU, True, "b", "b")])
+def test_linear_few_rows_many_features(M, N, K, act, bias, res, out):
+    # more CTAs than the SMs hold at once
+    test_linear(M, N, K, act, bias, res, out)
 
 
 @pytest.mark.parametrize("M,N,K", [(145, 2560, 512), (160, 2560, 512), (160, 300, 2563), (152, 9728, 256)])
