@@ -481,27 +481,31 @@ def zdit_qk_norm_rope(q, k, q_out, k_out, w_q, w_k, cos, sin, rotary_dim, layout
 class PromptBatch:
     """Lengths of the packed sequences of zdit_prompt_attention (host arrays, kept alive):
     q_len new rows each; kv_len keys each (None: q_len); kv_start first key row of each
-    (None: packed one after the other)."""
+    (None: packed one after the other).  Other lengths need another batch: the rows that a
+    call's tensors must have are counted here, once."""
 
     def __init__(self, q_len, kv_len=None, kv_start=None):
-        def arr(v):
+        def whole(v):
             if v is None:
                 return None
-            v = [int(x) for x in v]
+            v = tuple(int(x) for x in v)
             if any(not -2**31 <= x < 2**31 for x in v):  # (ctypes would keep the low 32 bits)
                 raise ValueError("PromptBatch: lengths and first rows must fit 32 bits")
-            return (C.c_int32 * len(v))(*v)
+            return v
 
+        q_len, kv_len, kv_start = whole(q_len), whole(kv_len), whole(kv_start)
         n = len(q_len)
         if any(v is not None and len(v) != n for v in (kv_len, kv_start)):
             raise ValueError("PromptBatch: q_len, kv_len and kv_start must have one entry per sequence")
-        self.batch = n
-        self.q_len, self.kv_len, self.kv_start = arr(q_len), arr(kv_len), arr(kv_start)
-        self._addr = tuple(0 if v is None else C.addressof(v) for v in (self.q_len, self.kv_len, self.kv_start))
-        self.q_rows = sum(self.q_len)
-        lens = list(self.q_len if kv_len is None else self.kv_len)
-        ends = [s + m for s, m in zip(self.kv_start, lens)] if kv_start is not None else [sum(lens)]
-        self.kv_rows = max(ends) if ends else 0
+        lens = q_len if kv_len is None else kv_len
+        ends = [sum(lens)] if kv_start is None else [s + m for s, m in zip(kv_start, lens)]
+        arrays = tuple(None if v is None else (C.c_int32 * n)(*v) for v in (q_len, kv_len, kv_start))
+        self.__dict__.update(batch=n, q_len=q_len, kv_len=kv_len, kv_start=kv_start, q_rows=sum(q_len),
+                             kv_rows=max(ends, default=0), _arrays=arrays,
+                             _addr=tuple(0 if v is None else C.addressof(v) for v in arrays))
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"PromptBatch: {name} cannot be set, make another batch")
 
     def args(self, n_heads, n_kv_heads, head_dim, causal, scale, heads=_NO_HEADS * 4):
         return _attn_args(self.batch, *self._addr, n_heads, n_kv_heads, head_dim, 1 if causal else 0, scale, *heads)

@@ -237,3 +237,20 @@ def test_batch_lengths_past_32_bits_are_refused(lens):
     # (kept modulo 2^32 they would be other rows)
     with pytest.raises(ValueError, match="PromptBatch"):
         Z.PromptBatch(**lens)
+
+
+def test_batch_cannot_change_after_its_rows_were_counted():
+    # the rows a batch needs are counted once; the library reads the lengths on every call
+    b = Z.PromptBatch([1, 2], [5, 6], [0, 9])
+    assert (list(b.q_len), list(b.kv_len), list(b.kv_start)) == ([1, 2], [5, 6], [0, 9])
+    for name in ("q_len", "kv_len", "kv_start"):
+        with pytest.raises(TypeError):
+            getattr(b, name)[0] = 1000
+        with pytest.raises(AttributeError):
+            setattr(b, name, [1000, 1000])
+    for name in ("batch", "q_rows", "kv_rows"):
+        with pytest.raises(AttributeError):
+            setattr(b, name, 1)
+    assert (b.batch, b.q_rows, b.kv_rows) == (2, 3, 15)
+    plain = Z.PromptBatch([3, 4])
+    assert plain.kv_len is None and plain.kv_start is None and plain.kv_rows == 7
