@@ -507,6 +507,9 @@ class PromptBatch:
     def __setattr__(self, name, value):
         raise AttributeError(f"PromptBatch: {name} cannot be set, make another batch")
 
+    def __reduce__(self):  # copies make arrays of their own
+        return PromptBatch, (self.q_len, self.kv_len, self.kv_start)
+
     def args(self, n_heads, n_kv_heads, head_dim, causal, scale, heads=_NO_HEADS * 4):
         return _attn_args(self.batch, *self._addr, n_heads, n_kv_heads, head_dim, 1 if causal else 0, scale, *heads)
 

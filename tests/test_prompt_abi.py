@@ -254,3 +254,18 @@ def test_batch_cannot_change_after_its_rows_were_counted():
     assert (b.batch, b.q_rows, b.kv_rows) == (2, 3, 15)
     plain = Z.PromptBatch([3, 4])
     assert plain.kv_len is None and plain.kv_start is None and plain.kv_rows == 7
+
+
+@pytest.mark.parametrize("how", ["copy", "deepcopy", "pickle"])
+def test_batch_copies_own_their_lengths(how):
+    # (addresses of the first one's arrays would outlive it, or mean nothing in another process)
+    import copy
+    import pickle
+    b = Z.PromptBatch([1, 2], [500, 600], [0, 900])
+    c = {"copy": copy.copy, "deepcopy": copy.deepcopy, "pickle": lambda x: pickle.loads(pickle.dumps(x))}[how](b)
+    old, new = b.args(4, 2, 128, True, 0.0), c.args(4, 2, 128, True, 0.0)
+    for name in ("q_len", "kv_len", "kv_start"):
+        x, y = getattr(old, name), getattr(new, name)
+        assert C.addressof(x.contents) != C.addressof(y.contents)
+        assert x[:2] == y[:2] == list(getattr(c, name))
+    assert (c.batch, c.q_rows, c.kv_rows) == (2, 3, 1500)
