@@ -368,10 +368,11 @@ ZDIT_API zdit_status zdit_gemm_bf16(const void* A, const void* B, float* C, int6
  * rotary tables of one position per token, per-head norms with either pairing of the
  * rotation, attention that is causal, has fewer key heads than query heads and runs over
  * prompts of different lengths packed one after the other, and projections that add
- * bias, activation and residual.  The four calls below are forward only, like the rest
- * of the library.  They return once their work is queued on the stream, need the tensors'
- * device to be the current one, and may be captured into graphs; zdit_profile_begin
- * records them under the kernel kinds that they resemble (rope_table, norm_modulate,
+ * bias, activation and residual.  The four calls below are those; the norm of a layer's rows
+ * and the product of a gated feed-forward's two halves are the caller's.  They are forward
+ * only, like the rest of the library.  They return once their work is queued on the stream,
+ * need the tensors' device to be the current one, may be captured into graphs, and may be
+ * made from several host threads at once; zdit_profile_begin records them under the kernel kinds that they resemble (rope_table, norm_modulate,
  * attention, gemm_embed_final). */
 
 /* Element types of the buffers whose type a call leaves open. */

@@ -407,7 +407,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 // UMMAs (1024 tensor clocks) per barrier wait instead of 4.  Measured per projection
 // (ncu, one main block): the gate/up GEMM runs its tensor pipe 94% of the time with
 // 128-deep slices against 89% with 64-deep ones; QKV and the out-projection (K = 3840)
-// lose 3-4 points with them; so the SwiGLU projection takes 128 and the others 64.
+// lose 3-4 points with them; so the SwiGLU projection takes 128 and the block's others 64.
+// EPI_LINEAR takes 128 as well (8351 x 3840 x 10240: 2% faster).
 template <int PBK>
 struct PairRing {
   static constexpr int BKP = PBK;

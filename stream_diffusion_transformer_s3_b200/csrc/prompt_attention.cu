@@ -16,14 +16,19 @@
 // TMEM columns: S buffers [0, 64) and [64, 128), O [128, +HD).  P (bf16 pairs) is written over
 // the first columns of its S and feeds the PV product from there.  Softmax in fp32: a running
 // maximum that moves only when a row grows by more than 16 (log2 units; P <= 2^16 keeps bf16's
-// relative precision), and the sum of the unrounded P.
+// relative precision), and the sum of the unrounded P.  P is rounded to bf16 because both operands
+// of a product have V's type (splitting it into two bf16 halves would double that product): the
+// outputs are then 1.8e-3 to 2.3e-3 off in the norm, against 1.5e-3 to 1.7e-3 for an fp32 P, where
+// only the stored result is rounded.
 // Per 128 x 64 unit the tensor core works 8 x 48 + 4 x 64 = 640 clocks (S reads both operands
 // from shared memory, 48 clocks a step instead of 32), the exponentials take 512, and shared
-// memory moves 32 KB of K and V in and 64 KB of operands out, 768: long prompts are bound
-// there (16384 tokens, 32 heads on 8: 2.0 to 2.1 ms, 1.05 to 1.1 PFLOP/s; under the power cap
-// 2.15 to 2.2 ms); a short item is mostly set-up, load latency and output (one key tile 4.3 us,
-// each further one 0.7 us), two of them at a time on an SM (24 captions of 8 to 512 tokens, 32
-// heads on 8: 34 us, 2.5 times the floor of their products and bytes).
+// memory moves 32 KB of K and V in and 64 KB of operands out, 768.  A unit of a long prompt
+// takes about 1120 clocks (16384 tokens, 32 heads on 8: tensor pipe 57% active, 2.0 to 2.1 ms,
+// 1.05 to 1.1 PFLOP/s; under the power cap 2.15 to 2.2 ms), so no unit is saturated: the rest
+// is the hand-over between softmax and MMA of the two CTAs.  A short item is mostly set-up, load
+// latency and output (one key tile 4.3 us, each further one 0.7 us), two of them at a time on an
+// SM (24 captions of 8 to 512 tokens, 32 heads on 8: 34 us, 2.5 times the floor of their products
+// and bytes).
 // Measured and not kept: two query tiles and 128-key tiles per CTA, one CTA per SM (half the K
 // and V traffic, but it waits for its own softmax: 1.0 to 1.6 times slower from 300 to 16384
 // tokens with 8 key heads); a persistent kernel that loads the next item while it finishes the
@@ -806,10 +811,14 @@ zdit_status launch_prompt(const CUtensorMap& tq, const CUtensorMap& tk, const CU
   {
     ProfScope ps(PROF_ATTENTION, 4.0 * HD * H * h.pairs,
                  2.0 * HD * (2.0 * H * h.q_rows + 2.0 * p.n_kv * h.kv_rows), s);
-    // Head after head keeps one head's keys in L2 while its items run (30 heads, 16 prompts of
-    // 300 tokens: 47 against 57 us); but with few waves the last head's longest items would end
-    // the launch alone, so then the longest items of all heads come first (8 heads, 2 prompts of
-    // 1024 tokens: 24 against 32 us).  Unmasked items are all alike.
+    // Head after head keeps one head's keys in L2 while its items run (30 heads, 16384 tokens: 2.08
+    // against 2.17 ms; 16 on 2, 2 of 8192: 504 against 529 us); but with few waves the last head's
+    // longest items would end the launch alone, so then the longest items of all heads come first
+    // (32 on 8, 2 prompts of 1024 tokens: 27 against 37 us; 8 heads, 2 of 4096: 70 against 106).
+    // Causal, 1 to 30 key heads, 1 to 120 prompts of 8 to 32768 tokens, time of head after head over
+    // heads first: 0.99 to 1.51 below 9 waves, 0.95 to 1.08 above but for one (30 heads, 120 of 300
+    // tokens: 1.32).  Unmasked items of a sequence are all alike (0.90 to 1.04; short prompts of 30
+    // heads 1.3).
     const int64_t items = h.p.item0[h.p.n];
     p.heads_first = p.causal && items * p.n_kv < 9 * (int64_t)num_sms();
     const dim3 grid = p.heads_first ? dim3((unsigned)p.n_kv, (unsigned)items) : dim3((unsigned)items, (unsigned)p.n_kv);
