@@ -372,8 +372,8 @@ ZDIT_API zdit_status zdit_gemm_bf16(const void* A, const void* B, float* C, int6
  * and the product of a gated feed-forward's two halves are the caller's.  They are forward
  * only, like the rest of the library.  They return once their work is queued on the stream,
  * need the tensors' device to be the current one, may be captured into graphs, and may be
- * made from several host threads at once; zdit_profile_begin records them under the kernel kinds that they resemble (rope_table, norm_modulate,
- * attention, gemm_embed_final). */
+ * made from several host threads at once; zdit_profile_begin records them under the kernel
+ * kinds that they resemble (rope_table, norm_modulate, attention, gemm_embed_final). */
 
 /* Element types of the buffers whose type a call leaves open. */
 enum { ZDIT_T_BF16 = 0, ZDIT_T_F32 = 1 };

@@ -976,3 +976,38 @@ def test_qk_norm_rope_several_tokens_in_place(rot):
 ])
 def test_rope_table_scaled_several_steps_a_cta(T, d, sc, first):
     test_rope_table_scaled(T, d, 1e6, sc, first)
+
+
+def test_prompt_layers_from_host_threads_at_once():
+    # every operator, from threads that each have a stream, buffers and lengths of their own
+    from concurrent.futures import ThreadPoolExecutor
+    from threading import Barrier
+    L = Layer(128, 4, 2, 64)
+    runs = []
+    for i, q_len in enumerate([(300, 7, 41), (1, 900), (5,), (64, 64, 2000)]):
+        T = sum(q_len)
+        x16 = rnd(30 + i, T, L.D)
+        pos = torch.cat([torch.arange(n) for n in q_len]).to(device="cuda", dtype=torch.int32)
+        buf = (torch.empty(T, 8 * 64, device="cuda", dtype=torch.bfloat16), torch.empty(T, 32, device="cuda"),
+               torch.empty(T, 32, device="cuda"), torch.empty(T, 4, 64, device="cuda", dtype=torch.bfloat16),
+               workspace(Z.PromptBatch(q_len), 4, 2, 64))
+        x = x16.float()
+        alone = torch.empty_like(x)
+        L.run(x, x16, pos, q_len, alone, buf)
+        runs.append((x, x16, pos, q_len, buf, alone, [torch.zeros_like(x) for _ in range(50)]))
+    torch.cuda.synchronize()
+    start = Barrier(len(runs), timeout=60)
+
+    def work(run):
+        x, x16, pos, q_len, buf, alone, outs = run
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            start.wait()
+            for o in outs:
+                L.run(x, x16, pos, q_len, o, buf)
+        stream.synchronize()
+        return all(torch.equal(o, alone) for o in outs)
+
+    with ThreadPoolExecutor(len(runs)) as pool:
+        assert all(pool.map(work, runs))
+    assert Z.zdit_device_status() == 0
